@@ -23,10 +23,17 @@ FA_ERR_MISALIGNED = 3
 FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
 FA_ERR_RANGE = 6
+FA_ERR_INDEX = 7
+FA_ERR_NO_PAGES = 8
+
+FA_BF16 = 0
+FA_F16 = 1
 
 EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_workspace_size", "fa_fwd_ws", "fa_fwd_f32", "fa_bwd_workspace_size", "fa_bwd", "fa_bwd_gqa_workspace_size",
            "fa_bwd_gqa", "fa_bwd_ws_workspace_size", "fa_bwd_ws", "fa_attn_fwd_workspace_size", "fa_attn_fwd", "fa_attn_bwd_workspace_size", "fa_attn_bwd",
            "fa_attn_fwd_fp8_workspace_size", "fa_attn_fwd_fp8", "fa_bwd_noalloc", "fa_last_device_status",
+           "fa_paged_attn_workspace_size", "fa_paged_attn", "fa_pages_write", "fa_pages_workspace_size", "fa_pages_copy",
+           "fa_pages_reserve", "fa_pages_fork", "fa_pages_free", "fa_pages_compact",
            "fa_device_status", "fa_bwd_set_phase_events", "fa_selftest_wait_timeout", "fa_selftest_exp2",
            "fa_status_str")
 
@@ -39,6 +46,28 @@ class FaAttnProblem(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("N", ctypes.c_int),
                 ("d", ctypes.c_int), ("scale", ctypes.c_float), ("causal", ctypes.c_int),
                 ("window_left", ctypes.c_int), ("window_right", ctypes.c_int)]
+
+
+class FaPagedProblem(ctypes.Structure):
+    """``fa_paged_problem`` of ``include/fa.h``."""
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("T", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("table_stride", ctypes.c_int),
+                ("prefix_len", ctypes.c_int), ("causal", ctypes.c_int), ("scale", ctypes.c_float),
+                ("k_stride", ctypes.c_longlong * 3), ("v_stride", ctypes.c_longlong * 3)]
+
+
+class FaPageTable(ctypes.Structure):
+    """``fa_page_table`` of ``include/fa.h``."""
+    _fields_ = [("rows", ctypes.c_int), ("max_pages", ctypes.c_int), ("table_stride", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("ref_counts", ctypes.c_void_p)]
+
+
+class FaPagePlanes(ctypes.Structure):
+    """``fa_page_planes`` of ``include/fa.h``."""
+    _fields_ = [("planes", ctypes.POINTER(ctypes.c_void_p)), ("n_planes", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_bytes", ctypes.c_longlong), ("page_stride", ctypes.c_longlong)]
 
 
 class FAError(RuntimeError):
@@ -100,6 +129,25 @@ def library() -> ctypes.CDLL:
     lib.fa_attn_fwd_fp8.restype = i
     lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp]
     lib.fa_bwd_noalloc.restype = i
+    pg, pt, pl = (ctypes.POINTER(t) for t in (FaPagedProblem, FaPageTable, FaPagePlanes))
+    lib.fa_paged_attn_workspace_size.argtypes = [pg]
+    lib.fa_paged_attn_workspace_size.restype = sz
+    lib.fa_paged_attn.argtypes = [pg, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.fa_paged_attn.restype = i
+    lib.fa_pages_write.argtypes = [pg, vp, vp, vp, vp, vp, vp, vp]
+    lib.fa_pages_write.restype = i
+    lib.fa_pages_workspace_size.argtypes = [i, i]
+    lib.fa_pages_workspace_size.restype = sz
+    lib.fa_pages_copy.argtypes = [pl, vp, vp, i, vp]
+    lib.fa_pages_copy.restype = i
+    lib.fa_pages_reserve.argtypes = [pt, vp, vp, sz, vp]
+    lib.fa_pages_reserve.restype = i
+    lib.fa_pages_fork.argtypes = [pl, pt, vp, vp, i, vp, sz, vp]
+    lib.fa_pages_fork.restype = i
+    lib.fa_pages_free.argtypes = [pt, vp, i, vp]
+    lib.fa_pages_free.restype = i
+    lib.fa_pages_compact.argtypes = [pl, pt, vp, vp, vp, vp, sz, vp]
+    lib.fa_pages_compact.restype = i
     lib.fa_selftest_wait_timeout.argtypes = [vp]
     lib.fa_selftest_wait_timeout.restype = i
     lib.fa_selftest_exp2.argtypes = [vp, vp, i, vp]
@@ -466,6 +514,290 @@ def fa_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, causal: bool = False, scale:
     return dq, dk, dv
 
 
+# ---- paged key/value cache.  These calls run on the tensors' device whatever the current one is.
+# With ``stream`` left out they run on that device's current stream; what they allocate themselves
+# belongs to the stream they run on.
+
+_PAGED_DTYPES = {torch.bfloat16: FA_BF16, torch.float16: FA_F16}
+
+
+def _launch_on(device: torch.device, stream, fn, *args) -> int:
+    if stream is not None and getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream_handle(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_handle(stream))
+
+
+def _empty_for(stream, shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
+    """An array for work on ``stream``: it is not handed out again before that work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        if not stream:  # the legacy default stream
+            stream = torch.cuda.default_stream(device)
+        else:
+            stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _cuda_device(t: torch.Tensor) -> torch.device:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    return t.device
+
+
+def _int32(name: str, t: torch.Tensor, device: torch.device, size: int | None = None) -> None:
+    """A dense 1-D int32 array on ``device``."""
+    if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or not t.is_contiguous() or \
+            (size is not None and t.numel() != size):
+        what = "" if size is None else f" of {size} elements"
+        raise ValueError(f"{name}: expected a contiguous 1-D int32 tensor{what} on {device}")
+
+
+def _table_dims(block_table: torch.Tensor, device: torch.device) -> tuple[int, int, int]:
+    """rows, max_pages and the row stride of a block table."""
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != device:
+        raise ValueError(f"block_table: expected a 2-D int32 tensor on {device}")
+    rows, width = block_table.shape
+    step = block_table.stride(0) if rows > 1 else width
+    if (width > 1 and block_table.stride(1) != 1) or step < width:
+        raise ValueError("block_table: the entries of a row must lie side by side and rows must not overlap")
+    return int(rows), int(width), int(step)
+
+
+def _pool_strides(pool: torch.Tensor) -> tuple[int, int, int]:
+    """Elements between pages, heads and tokens of a (num_pages, H_kv, page_size, d) pool."""
+    pages, heads, ps, d = pool.shape
+    s = pool.stride()
+    if pool.numel() and d > 1 and s[3] != 1:
+        raise ValueError("pages: the d elements of a token must lie side by side")
+    token = s[2] if ps > 1 else d  # the stride of a dimension of one element says nothing
+    head = s[1] if heads > 1 else ps * token
+    page = s[0] if pages > 1 else heads * ps * d
+    return (page, head, token) if pool.numel() else (heads * ps * d, ps * d, d)
+
+
+def _paged(q: torch.Tensor, k_pages, v_pages, block_table, H: int, H_kv: int, prefix_len=0, causal=True,
+           scale=None) -> FaPagedProblem:
+    device = _cuda_device(q)
+    if q.dtype not in _PAGED_DTYPES:
+        raise ValueError("expected bf16 or fp16 tensors")
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or int(k_pages.shape[1]) != H_kv or \
+            k_pages.shape[3] != q.shape[3]:
+        raise ValueError("k_pages and v_pages must be (num_pages, H_kv, page_size, d)")
+    for t in (k_pages, v_pages):
+        if t.dtype != q.dtype or t.device != device:
+            raise ValueError(f"expected pages of {q.dtype} on {device}")
+    rows, width, step = _table_dims(block_table, device)
+    B, T, d = int(q.shape[0]), int(q.shape[2]), int(q.shape[3])
+    if rows != B:
+        raise ValueError(f"block_table has {rows} rows for {B} sequences")
+    ll3 = ctypes.c_longlong * 3
+    return FaPagedProblem(B, H, H_kv, T, d, _PAGED_DTYPES[q.dtype], int(k_pages.shape[2]), int(k_pages.shape[0]), width,
+                          step, int(prefix_len), int(bool(causal)), _scale(scale, d),
+                          ll3(*_pool_strides(k_pages)), ll3(*_pool_strides(v_pages)))
+
+
+def paged_problem(q, k_pages, v_pages, block_table, prefix_len: int = 0, causal: bool = True,
+                  scale: float | None = None) -> FaPagedProblem:
+    """The ``fa_paged_problem`` of these tensors (as ``fa_paged_attn`` takes them)."""
+    H = _shape(q)[1]
+    H_kv = int(k_pages.shape[1]) if k_pages.dim() == 4 else 0
+    if H_kv < 1 or H % H_kv:
+        raise ValueError("k_pages must be (num_pages, H_kv, page_size, d), q's head count a multiple of H_kv")
+    return _paged(q, k_pages, v_pages, block_table, H, H_kv, prefix_len, causal, scale)
+
+
+def fa_paged_attn_workspace_size(problem: FaPagedProblem) -> int:
+    return int(library().fa_paged_attn_workspace_size(ctypes.byref(problem)))
+
+
+def fa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, prefix_table=None, prefix_len: int = 0,
+                  causal: bool = True, scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """Attention of the newest T tokens of every sequence over a paged cache (C ``fa_paged_attn``).
+
+    q (B, H, T, d) bf16 or fp16; k_pages, v_pages (num_pages, H_kv, page_size, d) with any strides
+    that keep a token's d elements together; block_table (B, max_pages) and seq_lens (B) int32;
+    prefix_table int32 with the pages of ``prefix_len`` tokens that all sequences share.  Returns
+    (o, lse).  Rows of negative length are left as they are in ``o`` and ``lse``."""
+    pr = paged_problem(q, k_pages, v_pages, block_table, prefix_len, causal, scale)
+    device = q.device
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _int32("seq_lens", seq_lens, device, pr.B)
+    if pr.prefix_len > 0:
+        if prefix_table is None:
+            raise ValueError("prefix_len needs a prefix_table")
+        _int32("prefix_table", prefix_table, device)
+        if prefix_table.numel() * pr.page_size < pr.prefix_len:
+            raise ValueError(f"prefix_table has {prefix_table.numel()} pages for {pr.prefix_len} tokens")
+    if o is None:
+        o = _empty_for(stream, q.shape, q.dtype, device)
+    if lse is None:
+        lse = _empty_for(stream, (pr.B, pr.H, pr.T), torch.float32, device)
+    _same(o, dtype=q.dtype, shape=q.shape)
+    _same(lse, dtype=torch.float32, shape=(pr.B, pr.H, pr.T))
+    if workspace is None:
+        workspace = _empty_for(stream, max(fa_paged_attn_workspace_size(pr), 1), torch.uint8, device)
+    if o.device != device or lse.device != device or workspace.device != device:
+        raise ValueError(f"expected o, lse and the workspace on {device}")
+    st = _launch_on(device, stream, library().fa_paged_attn, ctypes.byref(pr), q.data_ptr(), k_pages.data_ptr(),
+                    v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                    prefix_table.data_ptr() if pr.prefix_len > 0 else None, o.data_ptr(), lse.data_ptr(),
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _check("fa_paged_attn", st)
+    return o, lse
+
+
+def fa_pages_write(k, v, k_pages, v_pages, block_table, seq_lens, stream=None) -> None:
+    """Put k, v (B, H_kv, T, d), the T newest tokens of every sequence, into their pages (C
+    ``fa_pages_write``): token t of row b goes to position seq_lens[b] - T + t."""
+    B, H_kv, T, d = _shape(k)
+    pr = _paged(k, k_pages, v_pages, block_table, H_kv, H_kv)
+    _same(k, v, dtype=k.dtype, shape=(B, H_kv, T, d))
+    if v.device != k.device:
+        raise ValueError(f"expected v on {k.device}")
+    _int32("seq_lens", seq_lens, k.device, B)
+    st = _launch_on(k.device, stream, library().fa_pages_write, ctypes.byref(pr), k.data_ptr(), v.data_ptr(),
+                    k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr())
+    _check("fa_pages_write", st)
+
+
+def fa_pages_workspace_size(rows: int, num_pages: int) -> int:
+    return int(library().fa_pages_workspace_size(rows, num_pages))
+
+
+def _planes(planes) -> tuple[FaPagePlanes, torch.device]:
+    """``fa_page_planes`` of one (n_planes, num_pages, ...) tensor or of a sequence of
+    (num_pages, ...) tensors of one shape, type and layout; each page is dense."""
+    stacked = isinstance(planes, torch.Tensor)
+    if stacked and planes.dim() < 3:
+        raise ValueError("planes: expected a (n_planes, num_pages, ...) tensor")
+    tensors = [planes[0]] if stacked and planes.shape[0] else [] if stacked else list(planes)
+    if not tensors:
+        raise ValueError("planes: expected at least one plane")
+    x = tensors[0]
+    device = _cuda_device(x)
+    if x.dim() < 2:
+        raise ValueError("planes: expected (num_pages, ...) tensors")
+    size = 1
+    for n, step in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        if n > 1 and step != size:
+            raise ValueError("planes: the elements of a page must lie side by side")
+        size *= n
+    for t in tensors:
+        if t.shape != x.shape or t.dtype != x.dtype or t.stride() != x.stride() or t.device != device:
+            raise ValueError("planes: expected tensors of one shape, type, layout and device")
+    pages = int(x.shape[0])
+    esize = x.element_size()
+    if stacked:
+        apart = planes.stride(0) * esize
+        ptrs = [x.data_ptr() + i * apart for i in range(planes.shape[0])]
+    else:
+        ptrs = [t.data_ptr() for t in tensors]
+    array = (ctypes.c_void_p * len(ptrs))(*ptrs)
+    step = x.stride(0) if pages > 1 else size
+    if step < size:
+        raise ValueError("planes: pages must not overlap")
+    return FaPagePlanes(ctypes.cast(array, ctypes.POINTER(ctypes.c_void_p)), len(ptrs), pages, size * esize,
+                        step * esize), device
+
+
+def _page_table(page_size: int, block_table, seq_lens, ref_counts) -> tuple[FaPageTable, torch.device]:
+    device = _cuda_device(block_table)
+    rows, width, step = _table_dims(block_table, device)
+    _int32("seq_lens", seq_lens, device, rows)
+    _int32("ref_counts", ref_counts, device)
+    return FaPageTable(rows, width, step, int(page_size), ref_counts.numel(), block_table.data_ptr(),
+                       seq_lens.data_ptr(), ref_counts.data_ptr()), device
+
+
+def _pages_workspace(workspace, table: FaPageTable, device: torch.device, stream) -> torch.Tensor:
+    if workspace is None:
+        return _empty_for(stream, fa_pages_workspace_size(table.rows, table.num_pages), torch.uint8, device)
+    if workspace.device != device:
+        raise ValueError(f"expected the workspace on {device}")
+    return workspace
+
+
+def fa_pages_copy(planes, src, dst, stream=None) -> None:
+    """Page dst[i] = page src[i] in every plane (C ``fa_pages_copy``).  planes: one (n_planes,
+    num_pages, ...) tensor, or a sequence of (num_pages, ...) tensors (K and V of every layer)."""
+    pl, device = _planes(planes)
+    _int32("src", src, device)
+    _int32("dst", dst, device, src.numel())
+    st = _launch_on(device, stream, library().fa_pages_copy, ctypes.byref(pl), src.data_ptr(), dst.data_ptr(),
+                    src.numel())
+    _check("fa_pages_copy", st)
+
+
+def fa_pages_reserve(page_size: int, block_table, seq_lens, ref_counts, new_lens, workspace=None, stream=None) -> None:
+    """Pages for new_lens[b] tokens of every row b (C ``fa_pages_reserve``); updates block_table,
+    seq_lens and ref_counts."""
+    table, device = _page_table(page_size, block_table, seq_lens, ref_counts)
+    _int32("new_lens", new_lens, device, table.rows)
+    ws = _pages_workspace(workspace, table, device, stream)
+    st = _launch_on(device, stream, library().fa_pages_reserve, ctypes.byref(table), new_lens.data_ptr(), ws.data_ptr(),
+                    ws.numel() * ws.element_size())
+    _check("fa_pages_reserve", st)
+
+
+def fa_pages_fork(planes, page_size: int, block_table, seq_lens, ref_counts, parents, children, workspace=None,
+                  stream=None) -> None:
+    """Row children[i] continues from row parents[i] (C ``fa_pages_fork``): full pages are shared,
+    a partly filled last page is copied in every plane (planes as for ``fa_pages_copy``)."""
+    pl, device = _planes(planes)
+    table, table_device = _page_table(page_size, block_table, seq_lens, ref_counts)
+    if table_device != device:
+        raise ValueError(f"expected the table on {device}")
+    _int32("parents", parents, device)
+    _int32("children", children, device, parents.numel())
+    ws = _pages_workspace(workspace, table, device, stream)
+    st = _launch_on(device, stream, library().fa_pages_fork, ctypes.byref(pl), ctypes.byref(table), parents.data_ptr(),
+                    children.data_ptr(), parents.numel(), ws.data_ptr(), ws.numel() * ws.element_size())
+    _check("fa_pages_fork", st)
+
+
+def fa_pages_free(page_size: int, block_table, seq_lens, ref_counts, rows, stream=None) -> None:
+    """Take back the pages of the given rows (C ``fa_pages_free``)."""
+    table, device = _page_table(page_size, block_table, seq_lens, ref_counts)
+    _int32("rows", rows, device)
+    st = _launch_on(device, stream, library().fa_pages_free, ctypes.byref(table), rows.data_ptr(), rows.numel())
+    _check("fa_pages_free", st)
+
+
+def fa_pages_compact(planes, page_size: int, block_table, seq_lens, ref_counts, block_table_out=None,
+                     ref_counts_out=None, page_map=None, workspace=None, stream=None):
+    """Move the live pages to the front of the pool (C ``fa_pages_compact``; planes as for
+    ``fa_pages_copy``).  Returns (block_table_out, ref_counts_out, page_map); the first two may be
+    block_table and ref_counts themselves."""
+    pl, device = _planes(planes)
+    table, table_device = _page_table(page_size, block_table, seq_lens, ref_counts)
+    if table_device != device:
+        raise ValueError(f"expected the table on {device}")
+    if block_table_out is None:
+        block_table_out = _empty_for(stream, (table.rows, table.table_stride), torch.int32,
+                                     device)[:, :table.max_pages]
+    if ref_counts_out is None:
+        ref_counts_out = _empty_for(stream, table.num_pages, torch.int32, device)
+    if page_map is None:
+        page_map = _empty_for(stream, table.num_pages, torch.int32, device)
+    if _table_dims(block_table_out, device)[:2] != (table.rows, table.max_pages) or \
+            (table.rows > 1 and block_table_out.stride(0) != table.table_stride):
+        raise ValueError("block_table_out: expected the shape and row stride of block_table")
+    _int32("ref_counts_out", ref_counts_out, device, table.num_pages)
+    _int32("page_map", page_map, device, table.num_pages)
+    ws = _pages_workspace(workspace, table, device, stream)
+    st = _launch_on(device, stream, library().fa_pages_compact, ctypes.byref(pl), ctypes.byref(table),
+                    block_table_out.data_ptr(), ref_counts_out.data_ptr(), page_map.data_ptr(), ws.data_ptr(),
+                    ws.numel() * ws.element_size())
+    _check("fa_pages_compact", st)
+    return block_table_out, ref_counts_out, page_map
+
+
 def fa_selftest_wait_timeout(stream=None) -> None:
     """Enqueue the bounded-wait self-test (a wait that must give up after ~2 s and report
     FA_ERR_TIMEOUT through ``fa_device_status``)."""
@@ -484,7 +816,7 @@ def fa_selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:
 
 def fa_last_device_status(stream=None) -> int:
     """Synchronise and return (and clear) the device status code: FA_OK, FA_ERR_TIMEOUT,
-    FA_ERR_RANGE or FA_ERR_CUDA."""
+    FA_ERR_RANGE, FA_ERR_INDEX, FA_ERR_NO_PAGES or FA_ERR_CUDA."""
     return int(library().fa_last_device_status(_stream_handle(stream)))
 
 

@@ -8,6 +8,7 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
+#include "paged.h"
 
 namespace fa {
 
@@ -166,6 +167,15 @@ int* device_error_word() {
   return g_err_ptr[dev];
 }
 
+fa_status device_ready(int* num_sms, int** err) {
+  int dev = 0;
+  const fa_status st = device_setup(&dev);
+  if (st != FA_OK) return st;
+  *num_sms = g_num_sms[dev];
+  *err = g_err_ptr[dev];
+  return FA_OK;
+}
+
 bool make_tmap_3d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, int d, int N, int BH,
                   int box_cols, int box_rows, int swizzle_bytes) {
   if ((swizzle_bytes != 128 && swizzle_bytes != 64) || box_cols * elem_bytes != swizzle_bytes) return false;
@@ -196,6 +206,8 @@ const char* fa_status_str(fa_status s) {
     case FA_ERR_CUDA: return "FA_ERR_CUDA";
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
     case FA_ERR_RANGE: return "FA_ERR_RANGE";
+    case FA_ERR_INDEX: return "FA_ERR_INDEX";
+    case FA_ERR_NO_PAGES: return "FA_ERR_NO_PAGES";
   }
   return "FA_ERR_UNKNOWN";
 }
@@ -612,7 +624,7 @@ fa_status fa_last_device_status(fa_stream_t stream) {
   if (v != 0) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_fa_err_word, &zero, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-    return v == FA_ERR_RANGE ? FA_ERR_RANGE : FA_ERR_TIMEOUT;
+    return v >= FA_ERR_RANGE && v <= FA_ERR_NO_PAGES ? static_cast<fa_status>(v) : FA_ERR_TIMEOUT;
   }
   return FA_OK;
 }

@@ -77,7 +77,10 @@ typedef enum {
   FA_ERR_MISALIGNED = 3,  /* a tensor base address is not 16-byte aligned (TMA requirement) */
   FA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed (launch, tensor-map encode) */
   FA_ERR_TIMEOUT = 5,     /* a kernel gave up a bounded wait (reported by fa_last_device_status) */
-  FA_ERR_RANGE = 6        /* an input beyond the value range above (reported by fa_last_device_status) */
+  FA_ERR_RANGE = 6,       /* an input beyond the value range above (reported by fa_last_device_status) */
+  FA_ERR_INDEX = 7,       /* a page id, row, length or count in a device array out of its range, or entries that
+                             exclude one another (reported by fa_last_device_status) */
+  FA_ERR_NO_PAGES = 8     /* fewer free pages than asked for (reported by fa_last_device_status) */
 } fa_status;
 
 /*
@@ -339,9 +342,168 @@ FA_API fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, con
                                 int N, int d, float scale, int causal, fa_stream_t stream);
 
 /*
+ * Paged key/value cache
+ * ---------------------
+ * The entry points below serve sequences of different lengths from a pool of pages, and
+ * hold all the state of the cache in caller-owned device arrays, so that every call is
+ * asynchronous and can be captured in a graph:
+ *   k_pages, v_pages : (num_pages, H_kv, page_size, d) bf16 or fp16, one pool each per layer;
+ *                      any strides that are multiples of 8 elements, d innermost and dense.
+ *                      page_size is a power of two from 8 to 1024.
+ *   block_table      : int32 (rows, max_pages), `table_stride` elements between rows: entry e
+ *                      of row b names the page with tokens e * page_size ... of sequence b.
+ *   seq_lens         : int32 (rows): tokens of the row.  A negative length marks a row without
+ *                      a sequence.
+ *   ref_counts       : int32 (num_pages): how many table entries name the page.  A page is free
+ *                      exactly when its count is 0; pages are handed out lowest id first.
+ * Row b owns the entries e < ceil(max(seq_lens[b], 0) / page_size); entries behind them are
+ * never read.  num_pages is at most 2^20.  What the device arrays hold cannot be checked on the host: an entry out of its
+ * range is left out (never followed) and reported as FA_ERR_INDEX by fa_last_device_status.
+ */
+typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
+
+/*
+ * fa_paged_attn -- attention of the newest T tokens of every sequence over its pages, with a
+ * prefix that the whole batch shares (a system prompt, a document): the prefix's keys and
+ * values are read once for all sequences instead of once per sequence.
+ *   q, o            : (B, H, T, d) of `dtype`, 16-byte aligned, contiguous; lse: fp32 (B, H, T)
+ *                     or NULL.  T >= 1: 1 for decoding, more for drafts or a prompt's chunk.
+ *   block_table, seq_lens : of the B sequences; seq_lens[b] counts the sequence's own tokens,
+ *                     the T new ones included (their K, V are in the pages already) and the
+ *                     shared prefix not.
+ *   prefix_table    : int32 (ceil(prefix_len / page_size)) pages of the prefix; NULL if
+ *                     prefix_len is 0.
+ *   causal          : 1: query t sees own token j when j <= seq_lens[b] - T + t (the queries are
+ *                     the last T tokens); 0: every query sees all own tokens.  The prefix is
+ *                     visible to every query.
+ * Query head h reads key/value head h / (H / H_kv).  A query that sees no key gets o = 0 and
+ * lse = -inf.  Rows with seq_lens[b] < 0 are left as they were in o and lse.  Whatever lies in
+ * pages behind a sequence's last token (or behind prefix_len), infinities and NaN included, does
+ * not reach the outputs.
+ * Products run in `dtype` with fp32 accumulation, the softmax in fp32; the probabilities are
+ * rounded to `dtype` for the P V product (the row sum takes the rounded values), and o once at
+ * the end.  d is 64, 128 or 256.  The result does not depend on timing: partial sums are joined
+ * in a fixed order.
+ *   workspace       : fa_paged_attn_workspace_size(problem) bytes, 256-byte aligned; contents on
+ *                     entry do not matter; one call at a time per workspace.  The size depends
+ *                     on B, H, H_kv, T and d only, not on lengths.
+ */
+typedef struct fa_paged_problem {
+  int B, H, H_kv, T, d;
+  int dtype;                           /* fa_dtype */
+  int page_size, num_pages, max_pages; /* max_pages: entries of a block_table row */
+  int table_stride;                    /* elements between block_table rows, >= max_pages */
+  int prefix_len;
+  int causal;
+  float scale;
+  long long k_stride[3], v_stride[3]; /* elements between pages, heads and tokens */
+} fa_paged_problem;
+FA_API size_t fa_paged_attn_workspace_size(const fa_paged_problem* problem);
+FA_API fa_status fa_paged_attn(const fa_paged_problem* problem, const void* q, const void* k_pages,
+                               const void* v_pages, const int* block_table, const int* seq_lens,
+                               const int* prefix_table, void* o, float* lse, void* workspace,
+                               size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_pages_write -- puts the K and V of T new tokens per sequence into their pages: token t of
+ * row b goes to position seq_lens[b] - T + t (seq_lens counts the new tokens already, as in
+ * fa_paged_attn); tokens at a negative position and rows of negative length are skipped, so
+ * shorter prompts are aligned at the end of the T tokens.
+ *   problem : B, H_kv, T, d, dtype, the page and table sizes and the strides are used.
+ *   k, v    : (B, H_kv, T, d) of `dtype`, contiguous, 16-byte aligned.
+ * Rows must not share the page they write to.
+ */
+FA_API fa_status fa_pages_write(const fa_paged_problem* problem, const void* k, const void* v, void* k_pages,
+                                void* v_pages, const int* block_table, const int* seq_lens, fa_stream_t stream);
+
+/*
+ * The table of a cache as the page operations take it, and the memory behind its pages.
+ *   planes      : host array of n_planes device pointers: the pools that share one page numbering
+ *                 (K and V of every layer), each with page_bytes bytes per page, page_stride bytes
+ *                 apart; addresses, page_bytes and page_stride are multiples of 16.  n_planes <= 1024.
+ */
+typedef struct fa_page_table {
+  int rows, max_pages, table_stride, page_size, num_pages;
+  int* block_table;
+  int* seq_lens;
+  int* ref_counts;
+} fa_page_table;
+typedef struct fa_page_planes {
+  void* const* planes;
+  int n_planes;
+  int num_pages;
+  long long page_bytes, page_stride;
+} fa_page_planes;
+
+/*
+ * fa_pages_workspace_size -- device bytes that fa_pages_reserve, fa_pages_fork and fa_pages_compact
+ * need for a table of `rows` rows over `num_pages` pages (256-byte aligned, contents on entry do not
+ * matter, one call at a time).  0 for negative sizes.
+ */
+FA_API size_t fa_pages_workspace_size(int rows, int num_pages);
+
+/*
+ * fa_pages_copy -- page dst[i] = page src[i] in every plane, i < n (device int32 arrays).  Pairs
+ * with a negative id are skipped, and so are pairs with src[i] = dst[i].  A pair is left out, and
+ * FA_ERR_INDEX recorded, when an id is >= num_pages, when an earlier pair has the same dst, or
+ * when its dst is the src of another pair (the result would depend on the order).
+ */
+FA_API fa_status fa_pages_copy(const fa_page_planes* planes, const int* src, const int* dst, int n,
+                               fa_stream_t stream);
+
+/*
+ * fa_pages_reserve -- gives every row the pages for new_lens[b] tokens: a row with new_lens[b] >
+ * max(seq_lens[b], 0) gets ceil(new_lens[b] / page_size) - (entries it owns) of the lowest free
+ * pages, with count 1, and the length new_lens[b]; other rows stay as they are.  Rows are served in
+ * order: one is served only if all pages that it and the rows before it ask for are there,
+ * otherwise it stays as it was and FA_ERR_NO_PAGES is recorded.  A length that the table cannot
+ * hold leaves the row as it was (FA_ERR_INDEX).
+ *   new_lens : device int32 (rows).
+ */
+FA_API fa_status fa_pages_reserve(const fa_page_table* table, const int* new_lens, void* workspace,
+                                  size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_pages_fork -- makes row children[i] continue from row parents[i] (i < n, n <= rows): the child
+ * gets the parent's length and pages, whose counts grow; a last page that is only partly filled is
+ * copied, in every plane, to the lowest free page instead, so that both can go on writing.  Forks
+ * are served in order as in fa_pages_reserve (FA_ERR_NO_PAGES); one with a negative row is skipped;
+ * one is left out (FA_ERR_INDEX) when its rows are out of range or equal, when its parent has no
+ * sequence or its child still owns pages, when its parent is a child or its child a parent
+ * elsewhere in the list, or when an earlier fork has the same child.
+ */
+FA_API fa_status fa_pages_fork(const fa_page_planes* planes, const fa_page_table* table, const int* parents,
+                               const int* children, int n, void* workspace, size_t workspace_bytes,
+                               fa_stream_t stream);
+
+/*
+ * fa_pages_free -- takes the pages of rows[i], i < n, back: the counts of their pages go down by
+ * one, their entries become -1 and their lengths -1.  Negative rows, rows without a sequence and
+ * second mentions of a row are skipped; a row out of range, or an entry that names no counted
+ * page, is reported (FA_ERR_INDEX).
+ */
+FA_API fa_status fa_pages_free(const fa_page_table* table, const int* rows, int n, fa_stream_t stream);
+
+/*
+ * fa_pages_compact -- moves the live pages (count > 0) to the ids 0 .. n_live - 1, so that what lies
+ * behind them can be given back: the k-th live page with an id >= n_live goes to the k-th free id
+ * below it, in every plane; the others stay.
+ *   block_table_out, ref_counts_out : the table (rows, max_pages; rows table_stride apart) and the
+ *                 counts afterwards; they may be the arrays of `table` themselves.  Entries that no
+ *                 row owns are passed on as they are.
+ *   page_map    : int32 (num_pages): the new id of each page, -1 for free ones (for tables the
+ *                 caller keeps elsewhere, such as a prefix_table).
+ * The moved pages' old places keep their contents.
+ */
+FA_API fa_status fa_pages_compact(const fa_page_planes* planes, const fa_page_table* table, int* block_table_out,
+                                  int* ref_counts_out, int* page_map, void* workspace, size_t workspace_bytes,
+                                  fa_stream_t stream);
+
+/*
  * fa_last_device_status -- synchronises `stream`, then reports what the kernels of this
  * library on the current device recorded since the last call: FA_ERR_TIMEOUT (a bounded
- * wait gave up) or FA_ERR_RANGE (an input beyond the value range above); the word is
+ * wait gave up), FA_ERR_RANGE (an input beyond the value range above), FA_ERR_INDEX or
+ * FA_ERR_NO_PAGES (the paged cache); of several, the last one recorded.  The word is
  * then cleared.  FA_ERR_CUDA if the CUDA context holds an error, FA_OK otherwise.
  * fa_device_status is the same function under its earlier name.
  */

@@ -25,3 +25,4 @@ from .attention import (  # noqa: F401
     apply_window,
 )
 from .fp8 import e4m3_decode, attention_forward_fp8, attention_forward_fp8_rows  # noqa: F401
+from .paged import PageTable, paged_attention  # noqa: F401
