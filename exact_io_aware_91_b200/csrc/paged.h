@@ -72,22 +72,76 @@ cudaError_t launch_pages_compact_apply(const TableArgs& t, const PlanePtrs& pl, 
                                        int num_sms, uint8_t* ws, cudaStream_t s);
 
 // ------------------------------------------------------------------ attention over pages
+constexpr int kPagedMaxCtas = 148;  // persistent CTAs of the attention kernel (one per multiprocessor)
+
 struct PagedParams {
-  const void* q;
-  const void* k;
-  const void* v;
-  void* o;
-  float* lse;
   const int* table;
   const int* lens;
   const int* prefix_table;
-  long long ks[3], vs[3];  // elements between pages, heads, tokens
-  int B, H, H_kv, T;
+  void* o;
+  float* lse;
+  int B, H, H_kv, T, R;  // R = H / H_kv * T query rows share a key/value head: they lie side by side in q and o
   int page_shift, num_pages, max_pages, table_stride, prefix_len;
   int causal;
+  int box_rows;    // tokens per TMA box of K and V
+  int packed;      // 1: the prefix has work items of its own, each for the rows of several sequences
+  int seqs;        // packed: sequences per 128-row tile of a prefix item
+  int n_rc;        // row chunks of a (sequence, key/value head)
+  int n_groups;    // packed: prefix items per key/value head
+  int pre_tiles;   // key tiles of the prefix
+  int ctas;        // grid
   float scale_log2;
+  // partial results (unnormalised O, and the maximum and sum of each row), see PagedWs
+  int2* seg;       // own items: first and last part of the line that holds the item
+  float2* own_ml;
+  float* own_o;
+  float2* pre_ml;
+  float* pre_o;
   int* err;
 };
-cudaError_t launch_paged_attn(const PagedParams& p, int d, int dtype, cudaStream_t s);
+
+// Workspace of fa_paged_attn.  Own items are numbered (b * n_rc + rc) * H_kv + h, prefix items
+// h * n_groups + group.  An item that one CTA works on alone has the slot of its number (own items:
+// only when a prefix part has to be joined, otherwise the result is written at once); the part c of
+// the line that starts an item and does not end it has slot n_items + 2 c + 1, one that goes on with
+// an item begun in another part slot n_items + 2 c.
+struct PagedWs {
+  int item_rows;  // rows of an item: 256 (two 128-row tiles), d = 256: 128
+  int slot_rows;  // rows of an own slot
+  int packed, seqs, n_rc, n_groups;
+  long long own_items, own_slots, pre_items, pre_slots;
+  size_t off_seg, off_own_ml, off_own_o, off_pre_ml, off_pre_o, total;
+};
+inline PagedWs paged_ws_layout(int B, int H, int H_kv, int T, int d) {
+  auto align256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  PagedWs w{};
+  const long long R = (long long)H / H_kv * T;
+  w.item_rows = d == 256 ? 128 : 256;
+  w.packed = R <= 128;
+  w.seqs = w.packed ? (int)(128 / R) : 1;
+  w.n_rc = (int)((R + w.item_rows - 1) / w.item_rows);
+  w.slot_rows = (int)(R < w.item_rows ? R : w.item_rows);
+  const int per_group = w.seqs * (w.item_rows / 128);  // sequences per prefix item
+  w.n_groups = w.packed ? (B + per_group - 1) / per_group : 0;
+  w.own_items = (long long)B * w.n_rc * H_kv;
+  w.own_slots = (w.packed ? w.own_items : 0) + 2 * kPagedMaxCtas;
+  w.pre_items = (long long)w.n_groups * H_kv;
+  w.pre_slots = w.packed ? w.pre_items + 2 * kPagedMaxCtas : 0;
+  w.off_seg = 0;
+  w.off_own_ml = align256((size_t)w.own_items * sizeof(int2));
+  w.off_own_o = w.off_own_ml + align256((size_t)w.own_slots * w.slot_rows * sizeof(float2));
+  w.off_pre_ml = w.off_own_o + align256((size_t)w.own_slots * w.slot_rows * d * sizeof(float));
+  w.off_pre_o = w.off_pre_ml + align256((size_t)w.pre_slots * w.item_rows * sizeof(float2));
+  w.total = w.off_pre_o + align256((size_t)w.pre_slots * w.item_rows * d * sizeof(float));
+  return w;
+}
+
+struct PagedMaps {
+  CUtensorMap q_own, q_pre, k, v;
+};
+// (64 columns x rows) boxes with the 128-byte swizzle over a 4-D 16-bit tensor; strides in bytes
+bool make_tmap_4d(CUtensorMap* m, const void* base, bool bf16, const unsigned long long (&dims)[4],
+                  const unsigned long long (&strides)[3], const unsigned (&box)[4]);
+cudaError_t launch_paged_attn(const PagedMaps& maps, const PagedParams& p, int d, int dtype, cudaStream_t s);
 
 }  // namespace fa

@@ -118,7 +118,7 @@ extern "C" {
 size_t fa_paged_attn_workspace_size(const fa_paged_problem* pr) {
   bool empty = false;
   if (check_paged(pr, true, &empty) != FA_OK || empty) return 0;
-  return 256;
+  return paged_ws_layout(pr->B, pr->H, pr->H_kv, pr->T, pr->d).total;
 }
 
 fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k_pages, const void* v_pages,
@@ -137,30 +137,62 @@ fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k
   PagedParams p{};
   int num_sms = 0;
   if ((st = device_ready(&num_sms, &p.err)) != FA_OK) return st;
-  p.q = q;
-  p.k = k_pages;
-  p.v = v_pages;
-  p.o = o;
-  p.lse = lse;
+  const PagedWs w = paged_ws_layout(pr->B, pr->H, pr->H_kv, pr->T, pr->d);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const int d = pr->d, tile_keys = d == 256 ? 64 : 128;
   p.table = block_table;
   p.lens = seq_lens;
   p.prefix_table = prefix_table;
-  for (int i = 0; i < 3; ++i) {
-    p.ks[i] = pr->k_stride[i];
-    p.vs[i] = pr->v_stride[i];
-  }
+  p.o = o;
+  p.lse = lse;
   p.B = pr->B;
   p.H = pr->H;
   p.H_kv = pr->H_kv;
   p.T = pr->T;
+  p.R = pr->H / pr->H_kv * pr->T;
   p.page_shift = page_shift(pr->page_size);
   p.num_pages = pr->num_pages;
   p.max_pages = pr->max_pages;
   p.table_stride = pr->table_stride;
   p.prefix_len = pr->prefix_len;
   p.causal = pr->causal;
+  p.box_rows = std::min(pr->page_size, 32);
+  p.packed = w.packed;
+  p.seqs = w.seqs;
+  p.n_rc = w.n_rc;
+  p.n_groups = w.n_groups;
+  p.pre_tiles = (pr->prefix_len + tile_keys - 1) / tile_keys;
+  p.ctas = std::min(num_sms, kPagedMaxCtas);
   p.scale_log2 = pr->scale * 1.4426950408889634f;
-  return to_status(launch_paged_attn(p, pr->d, pr->dtype, reinterpret_cast<cudaStream_t>(stream)));
+  p.seg = reinterpret_cast<int2*>(ws + w.off_seg);
+  p.own_ml = reinterpret_cast<float2*>(ws + w.off_own_ml);
+  p.own_o = reinterpret_cast<float*>(ws + w.off_own_o);
+  p.pre_ml = reinterpret_cast<float2*>(ws + w.off_pre_ml);
+  p.pre_o = reinterpret_cast<float*>(ws + w.off_pre_o);
+
+  typedef unsigned long long u64;
+  const bool bf = pr->dtype == FA_BF16;
+  PagedMaps maps;
+  // q as (d, R rows, H_kv, B): a box takes the same rows of one sequence (own items) or of
+  // p.seqs consecutive sequences (prefix items)
+  const u64 row = 2ull * d, qd[4] = {(u64)d, (u64)p.R, (u64)p.H_kv, (u64)p.B};
+  const u64 qs[3] = {row, row * p.R, row * p.R * p.H_kv};
+  const unsigned box_q = (unsigned)std::min(p.R, 128);
+  const unsigned own_box[4] = {64, box_q, 1, 1}, pre_box[4] = {64, box_q, 1, (unsigned)p.seqs};
+  const unsigned kv_box[4] = {64, (unsigned)p.box_rows, 1, 1};
+  // pages: (d, page_size, H_kv, num_pages); the page id after the last one reads zeros
+  const u64 kd[4] = {(u64)d, (u64)pr->page_size, (u64)p.H_kv, (u64)std::max(p.num_pages, 1)};
+  u64 ks[3], vs[3];
+  for (int i = 0; i < 3; ++i) {
+    ks[i] = 2ull * pr->k_stride[2 - i];
+    vs[i] = 2ull * pr->v_stride[2 - i];
+  }
+  const void* kb = p.num_pages > 0 ? k_pages : q;
+  const void* vb = p.num_pages > 0 ? v_pages : q;
+  if (!make_tmap_4d(&maps.q_own, q, bf, qd, qs, own_box) || !make_tmap_4d(&maps.q_pre, q, bf, qd, qs, pre_box) ||
+      !make_tmap_4d(&maps.k, kb, bf, kd, ks, kv_box) || !make_tmap_4d(&maps.v, vb, bf, kd, vs, kv_box))
+    return FA_ERR_CUDA;
+  return to_status(launch_paged_attn(maps, p, d, pr->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 fa_status fa_pages_write(const fa_paged_problem* pr, const void* k, const void* v, void* k_pages, void* v_pages,

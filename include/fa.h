@@ -357,8 +357,10 @@ FA_API fa_status fa_bwd_noalloc(const void* q, const void* k, const void* v, con
  *   ref_counts       : int32 (num_pages): how many table entries name the page.  A page is free
  *                      exactly when its count is 0; pages are handed out lowest id first.
  * Row b owns the entries e < ceil(max(seq_lens[b], 0) / page_size); entries behind them are
- * never read.  num_pages is at most 2^20.  What the device arrays hold cannot be checked on the host: an entry out of its
- * range is left out (never followed) and reported as FA_ERR_INDEX by fa_last_device_status.
+ * never read.  num_pages is at most 2^20.  What the device arrays hold cannot be checked on the
+ * host: an entry out of its range is never followed but reported as FA_ERR_INDEX by
+ * fa_last_device_status (fa_paged_attn then takes zeros for the page's keys and values, and of a
+ * length that the table cannot hold as much as it holds).
  */
 typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
 
@@ -503,7 +505,7 @@ FA_API fa_status fa_pages_compact(const fa_page_planes* planes, const fa_page_ta
  * fa_last_device_status -- synchronises `stream`, then reports what the kernels of this
  * library on the current device recorded since the last call: FA_ERR_TIMEOUT (a bounded
  * wait gave up), FA_ERR_RANGE (an input beyond the value range above), FA_ERR_INDEX or
- * FA_ERR_NO_PAGES (the paged cache); of several, the last one recorded.  The word is
+ * FA_ERR_NO_PAGES (the paged cache); of several, one of them.  The word is
  * then cleared.  FA_ERR_CUDA if the CUDA context holds an error, FA_OK otherwise.
  * fa_device_status is the same function under its earlier name.
  */

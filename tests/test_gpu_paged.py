@@ -180,7 +180,8 @@ def test_rows_without_a_sequence_are_left_as_they_were():
 def test_repeated_calls_are_identical_and_need_nothing_of_the_workspace():
     c = Cache([700, 31, 1200], 900, 4, 128, 16, BF16, seed=2)
     q = c.queries(16, 1)
-    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    pr = api.paged_problem(q, c.k, c.v, torch.from_numpy(c.table).cuda(), 900)
+    ws = torch.empty(api.fa_paged_attn_workspace_size(pr), dtype=torch.uint8, device="cuda")
     ref = None
     for fill in (0, 255, 77):
         ws.fill_(fill)
