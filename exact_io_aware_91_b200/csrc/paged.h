@@ -73,6 +73,8 @@ cudaError_t launch_pages_compact_apply(const TableArgs& t, const PlanePtrs& pl, 
 
 // ------------------------------------------------------------------ attention over pages
 constexpr int kPagedMaxCtas = 148;  // persistent CTAs of the attention kernel (one per multiprocessor)
+constexpr int kFewRows = 32;        // items of at most this many rows take the products with swapped operands
+constexpr int kItemCost = 1;        // an item's own cost in the division of the line, in key tiles
 
 struct PagedParams {
   const int* table;
@@ -85,9 +87,11 @@ struct PagedParams {
   int causal;
   int box_rows;    // tokens per TMA box of K and V
   int packed;      // 1: the prefix has work items of its own, each for the rows of several sequences
+  int own_few, pre_few;  // own / prefix items have at most kFewRows rows
   int seqs;        // packed: sequences per 128-row tile of a prefix item
   int n_rc;        // row chunks of a (sequence, key/value head)
   int n_groups;    // packed: prefix items per key/value head
+  int own_kt, pre_kt;  // log2 of the keys per tile
   int pre_tiles;   // key tiles of the prefix
   int ctas;        // grid
   float scale_log2;
@@ -108,7 +112,7 @@ struct PagedParams {
 struct PagedWs {
   int item_rows;  // rows of an item: 256 (two 128-row tiles), d = 256: 128
   int slot_rows;  // rows of an own slot
-  int packed, seqs, n_rc, n_groups;
+  int packed, own_few, pre_few, seqs, n_rc, n_groups;
   long long own_items, own_slots, pre_items, pre_slots;
   size_t off_seg, off_own_ml, off_own_o, off_pre_ml, off_pre_o, total;
 };
@@ -118,11 +122,13 @@ inline PagedWs paged_ws_layout(int B, int H, int H_kv, int T, int d) {
   const long long R = (long long)H / H_kv * T;
   w.item_rows = d == 256 ? 128 : 256;
   w.packed = R <= 128;
-  w.seqs = w.packed ? (int)(128 / R) : 1;
+  w.own_few = R <= kFewRows;
+  w.pre_few = R * B <= kFewRows;  // the rows of the whole batch
+  w.seqs = w.pre_few ? B : w.packed ? (int)(128 / R) : 1;
   w.n_rc = (int)((R + w.item_rows - 1) / w.item_rows);
   w.slot_rows = (int)(R < w.item_rows ? R : w.item_rows);
   const int per_group = w.seqs * (w.item_rows / 128);  // sequences per prefix item
-  w.n_groups = w.packed ? (B + per_group - 1) / per_group : 0;
+  w.n_groups = !w.packed ? 0 : w.pre_few ? 1 : (B + per_group - 1) / per_group;
   w.own_items = (long long)B * w.n_rc * H_kv;
   w.own_slots = (w.packed ? w.own_items : 0) + 2 * kPagedMaxCtas;
   w.pre_items = (long long)w.n_groups * H_kv;

@@ -139,7 +139,7 @@ fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k
   if ((st = device_ready(&num_sms, &p.err)) != FA_OK) return st;
   const PagedWs w = paged_ws_layout(pr->B, pr->H, pr->H_kv, pr->T, pr->d);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int d = pr->d, tile_keys = d == 256 ? 64 : 128;
+  const int d = pr->d;
   p.table = block_table;
   p.lens = seq_lens;
   p.prefix_table = prefix_table;
@@ -161,7 +161,11 @@ fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k
   p.seqs = w.seqs;
   p.n_rc = w.n_rc;
   p.n_groups = w.n_groups;
-  p.pre_tiles = (pr->prefix_len + tile_keys - 1) / tile_keys;
+  p.own_few = w.own_few;
+  p.pre_few = w.pre_few;
+  p.own_kt = w.own_few || d != 256 ? 7 : 6;  // 128 keys; two 128-row tiles at d = 256 leave room for 64
+  p.pre_kt = w.pre_few || d != 256 ? 7 : 6;
+  p.pre_tiles = (pr->prefix_len + (1 << p.pre_kt) - 1) >> p.pre_kt;
   p.ctas = std::min(num_sms, kPagedMaxCtas);
   p.scale_log2 = pr->scale * 1.4426950408889634f;
   p.seg = reinterpret_cast<int2*>(ws + w.off_seg);

@@ -14,23 +14,28 @@
 // one sequence fill tiles by themselves: then own items go over the prefix keys first and there are
 // no prefix items.
 //
-// Split.  A unit is one item and one key tile (128 keys; d = 256: 64).  The units of all own items
-// are one line, cut into equal parts for the persistent CTAs (one per multiprocessor), and so are
-// those of the prefix items; a CTA walks its part of both lines.  So ragged lengths load all
-// multiprocessors equally, without the host knowing them: every CTA adds up the lengths itself.  A part
-// that covers an item only partly leaves (m, l, O) in the workspace, and a second kernel joins
+// Split.  A unit is one item and one tile of 128 keys (64 in the dense form at d = 256).  The units of
+// all own items are one line, cut into equal parts for the persistent CTAs (one per multiprocessor),
+// and so are those of the prefix items; a CTA walks its part of both lines.  So ragged lengths load
+// all multiprocessors equally, without the host knowing them: every CTA adds up the lengths itself.
+// A part that covers an item only partly leaves (m, l, O) in the workspace, and a second kernel joins
 // the parts of each row in the order of the line (the same on every run).  CTAs with an odd
 // number walk the own line first: own items wait for memory (each key is used for R rows only),
 // prefix items for the tensor core, and the two overlap across the device.
 //
-// In a CTA: warp 0 looks up pages and streams K and V tiles with TMA into a ring, one box per
-// piece of a page (16 to 32 lanes issue one box each); warp 1 issues the tensor-core products, S of
-// a step two steps ahead of its P V, across items; two warpgroups of softmax warps take the steps
-// in turn, each with an S (then P) buffer and an O accumulator of its own in tensor memory.  With
-// two query tiles a key tile is two steps, one per tile; with one tile the warpgroups take
-// alternate key tiles and join their two partial results in the end.  A single query row costs a
-// 128-row product: at 128 keys 0.5 us of tensor core against 1.5 us that a multiprocessor's share
-// of the memory bandwidth takes for the keys, so the padding is not what bounds it.
+// Two forms of a tile's products:
+//   dense  S = Q K^T and O += P V with the query rows as the 128 rows of the product, for items of
+//          more than 32 rows: two softmax warpgroups, one thread per row, take the steps in turn.
+//   few    S^T = K Q^T and O^T += V^T P^T with the keys, then the columns of V, as the 128 rows and
+//          the (up to 32) query rows as columns.  One thread per key then has one weight per query
+//          row to compute instead of 128, all four warps work, and the rows of O^T are the elements
+//          of o that are stored side by side.  With the dense form a step of a few rows took 2500
+//          cycles (one warp's 128 exponentials) and its epilogue 2700, where a tile's share of the
+//          memory bandwidth is 1400 (d = 64) or 2800.
+// In both, warp 0 looks up pages and streams Q and K tiles with TMA, warp 2 V tiles, into one ring (a
+// lane issues the box of a piece of a page; two warps, because a box costs its issuer some 70
+// cycles and 8-token pages make 32 of them per tile), and warp 1 issues the tensor-core products, S
+// of a step two steps ahead of its P V, across items.
 //
 // What lies behind a sequence's last token in a page never enters: its scores are masked, and the rows of
 // the V tile are set to zero in shared memory (0 x NaN would be NaN).  P is rounded to the 16-bit
@@ -45,8 +50,14 @@
 namespace fa {
 namespace {
 
+constexpr int kThreads = 384;  // warp 0: Q, K; 1: products; 2: V; 4-7 and 8-11: softmax
+// registers: the first four warps give theirs to the two softmax warpgroups
+constexpr uint32_t kRegsLaunch = 168, kRegsLow = 88, kRegsHigh = 208;
+static_assert(kRegsLow + 2 * kRegsHigh <= 3 * kRegsLaunch, "register split exceeds the launch budget");
+
+// Shared memory and tensor memory of the dense form.
 template <int D>
-struct PLayout {
+struct Dense {
   static constexpr int KT = D == 256 ? 64 : 128;     // keys per tile
   static constexpr int NWG = D == 256 ? 1 : 2;       // softmax warpgroups = O accumulators = query tiles
   static constexpr int KCH = D / 64;                 // 128-byte column chunks per row
@@ -55,35 +66,56 @@ struct PLayout {
   static constexpr int CHUNK = KT * 128;             // one chunk of a K or V tile
   static constexpr int SLOT = KCH * CHUNK;
   static constexpr int NS = D == 64 ? 12 : 5;        // ring slots
-  static constexpr int THREADS = 128 + 128 * NWG;
   static constexpr int OFF_KV = NWG * QTILE;
   static constexpr int OFF_STAT = OFF_KV + NS * SLOT;  // float2[128]: a warpgroup's m and l for the other
-  static constexpr int OFF_BAR = OFF_STAT + 1024;
-  static constexpr int BAR_Q_FULL = 0;                 // [2]
-  static constexpr int BAR_Q_EMPTY = 2;                // [2]
-  static constexpr int BAR_S_FULL = 4;                 // [2]
-  static constexpr int BAR_P_FULL = 6;                 // [2]
-  static constexpr int BAR_O_FULL = 8;                 // [2]
-  static constexpr int BAR_O_FREE = 10;                // [2]
-  static constexpr int BAR_STAT_FULL = 12, BAR_STAT_EMPTY = 13, BAR_PV_DONE = 14, BAR_MMA_DONE = 15;
-  static constexpr int BAR_KV_FULL = 16;               // [NS]
-  static constexpr int BAR_KV_EMPTY = 16 + NS;         // [NS]
-  static constexpr int NBAR = 16 + 2 * NS;
-  static constexpr int OFF_START = OFF_BAR + NBAR * 8; // Start
-  static constexpr int OFF_SCAN = OFF_START + 48;      // long long[12]
-  static constexpr int OFF_TMEM_SLOT = OFF_SCAN + 96;
-  static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
-  static constexpr int SMEM_ALLOC = OFF_ABORT + 8 + 1024;
-  static_assert(SMEM_ALLOC <= 232448, "shared memory per CTA");
+  static constexpr int END = OFF_STAT + 1024;
+  static constexpr int HALVES = KT / 64;               // P is handed over in parts of 64 keys
+  // barriers
+  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6 /* [2][2] */, O_FULL = 10, O_FREE = 12;
+  static constexpr int STAT_FULL = 14, STAT_EMPTY = 15, PV_DONE = 16, MMA_DONE = 17, KV_FULL = 18, KV_EMPTY = 18 + NS;
+  static constexpr int NBAR = 18 + 2 * NS;
   static_assert(NS >= 4, "S of a step is issued two steps ahead: two K and two V tiles are held at once");
   static __host__ __device__ constexpr uint32_t T_S(int i) { return i * KT; }
   static __host__ __device__ constexpr uint32_t T_O(int i) { return 256 + i * D; }
   static_assert(2 * KT <= 256 && 256 + NWG * D <= 512, "tensor memory columns");
 };
 
-// registers: the producer and product warps give theirs to the two softmax warpgroups
-constexpr uint32_t kRegsLaunch = 168, kRegsLow = 72, kRegsHigh = 216;
-static_assert(kRegsLow + 2 * kRegsHigh <= 3 * kRegsLaunch, "register split exceeds the launch budget");
+// The same of the few-rows form.  A ring slot holds 128 keys x up to 128 columns.
+template <int D>
+struct Few {
+  static constexpr int KCH = D / 64;
+  static constexpr int PARTS = D == 256 ? 2 : 1;     // slots per K or V tile
+  static constexpr int PCH = KCH / PARTS;            // chunks per slot
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int SLOT = PCH * CHUNK;
+  static constexpr int NS = D == 64 ? 11 : 5;
+  static constexpr int NQ = D == 256 ? 2 : 4;        // query buffers
+  static constexpr int RCHUNK = kFewRows * 128;      // one chunk (64 columns or keys) of Q or P^T
+  static constexpr int OFF_Q = NS * SLOT;
+  static constexpr int OFF_P = OFF_Q + NQ * KCH * RCHUNK;  // [2] buffers of 32 rows x 128 keys
+  static constexpr int OFF_EX = OFF_P + 2 * 2 * RCHUNK;    // float[2 warpgroups][2][32][4]
+  static constexpr int END = OFF_EX + 2048;
+  // the product of d = 64 takes 128 columns of V: the second 64 are whatever follows the slot
+  static_assert(D != 64 || OFF_Q + CHUNK <= END, "the last slot's neighbour is inside shared memory");
+  static constexpr int Q_FULL = 0, Q_EMPTY = NQ, S_FULL = 2 * NQ, P_FULL = S_FULL + 4, P_EMPTY = P_FULL + 2;
+  static constexpr int O_FULL = P_EMPTY + 2, O_FREE = O_FULL + 2, MMA_DONE = O_FREE + 2, KV_FULL = MMA_DONE + 1;
+  static constexpr int KV_EMPTY = KV_FULL + NS, NBAR = KV_EMPTY + NS;
+  static __host__ __device__ constexpr uint32_t T_S(int i) { return i * kFewRows; }                          // [4]
+  static __host__ __device__ constexpr uint32_t T_O(int i, int h) { return 128 + (i * 2 + h) * kFewRows; }   // [2][2]
+};
+
+constexpr int cmax(int a, int b) { return a > b ? a : b; }
+template <int D>
+struct Smem {
+  static constexpr int OFF_BAR = cmax(Dense<D>::END, Few<D>::END);
+  static constexpr int DENSE_BAR = 0, FEW_BAR = Dense<D>::NBAR;
+  static constexpr int OFF_START = OFF_BAR + (Dense<D>::NBAR + Few<D>::NBAR) * 8;
+  static constexpr int OFF_SCAN = OFF_START + 48;  // long long[12]
+  static constexpr int OFF_TMEM_SLOT = OFF_SCAN + 96;
+  static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
+  static constexpr int ALLOC = OFF_ABORT + 8 + 1024;
+  static_assert(ALLOC <= 232448, "shared memory per CTA");
+};
 
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
@@ -101,7 +133,74 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-__device__ __forceinline__ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+// N = 8, 16 or 32 consecutive columns of this warp's 32 lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "column counts in use");
+  if constexpr (N == 32) {
+    tmem_ld32(taddr, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  } else {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) {
+  if constexpr (N == 32)
+    tmem_st32(taddr, r);
+  else if constexpr (N == 16)
+    tmem_st16(taddr, r);
+  else
+    tmem_st8(taddr, r);
+}
+
+__device__ __forceinline__ float warp_max(float x) {  // over the 32 lanes
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Whether any of the 128 threads of a warpgroup says so; a barrier among them as well.
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) { named_bar_sync((uint32_t)id, 128); }
+
+__device__ __forceinline__ void st_global_32b(void* dst, const uint32_t* v) {  // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  return BF ? pack_bf16(a, b) : pack_f16(a, b);
+}
+template <bool BF>
+__device__ __forceinline__ uint16_t round16(float a) {
+  if constexpr (BF)
+    return __bfloat16_as_ushort(__float2bfloat16_rn(a));
+  else
+    return __half_as_ushort(__float2half_rn(a));
+}
+__device__ __forceinline__ float log_sum(float m, float l) {  // natural logarithm of 2^m l
+  return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
 
 // ---------------------------------------------------------------------------- the two lines of units
 // Own tokens of sequence b, at most what its row of the table holds; negative: no sequence.
@@ -122,18 +221,18 @@ __device__ __forceinline__ int own_visible(const PagedParams& p, int len, int rc
 }
 
 // Key tiles of an own item: the prefix's first where it has no items of its own.
-template <int KT>
 __device__ __forceinline__ int own_tiles(const PagedParams& p, int len, int visible) {
   if (len < 0) return 0;
-  return (p.packed ? 0 : p.pre_tiles) + (visible + KT - 1) / KT;
+  return (p.packed ? 0 : p.pre_tiles) + ((visible + (1 << p.own_kt) - 1) >> p.own_kt);
 }
+// Length of an item on the line: kItemCost for its beginning and end, then its tiles.
+__device__ __forceinline__ int item_units(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
 
-template <int D>
+template <int ITEM>
 __device__ long long units_of(const PagedParams& p, int b) {
-  using L = PLayout<D>;
   const int len = own_len(p, b);
   long long n = 0;
-  for (int rc = 0; rc < p.n_rc; ++rc) n += own_tiles<L::KT>(p, len, own_visible<128 * L::NWG>(p, len, rc));
+  for (int rc = 0; rc < p.n_rc; ++rc) n += item_units(own_tiles(p, len, own_visible<ITEM>(p, len, rc)));
   return n * p.H_kv;
 }
 
@@ -151,92 +250,83 @@ __device__ __forceinline__ int part_of(long long n, int parts, long long u) {
 struct Start {  // where a CTA's part of the own line begins
   long long total;  // units of the whole line
   long long left;   // units of this CTA
-  int b, rc, hk, tile;
+  int b, rc, hk, at;  // item, and the unit inside it
 };
 
 // One item, or the part of it that falls into a CTA's part of the line.
 struct Seg {
   bool own;
-  int b, rc, hk;    // prefix: b is the first sequence of tile 0
-  int len;          // own: the sequence's length
-  int visible;      // own: keys seen by some row
-  int t0, t1, nt;   // key tiles t0 .. t1 - 1 of nt
-  bool pair;        // two query tiles
-  int steps;
+  int b, rc, hk;   // prefix: b is the first sequence of tile 0
+  int len;         // own: the sequence's length
+  int visible;     // own: keys seen by some row
+  int t0, t1, nt;  // key tiles t0 .. t1 - 1 of nt
+  bool pair;       // dense: two query tiles
 };
 
-// Walks a CTA's segments; every role does so for itself.
-template <int D>
+// Walks a CTA's segments of one line or both; every role does so for itself.
+template <int ITEM>
 struct Walk {
-  using L = PLayout<D>;
   const PagedParams& p;
   long long pre_u, pre_end, own_left;
-  int b, rc, hk, tile;
-  int cur_b;
-  int len;
+  int b, rc, hk, at;
+  int cur_b, len;
   bool own_first;
 
-  __device__ Walk(const PagedParams& p_, const Start& s) : p(p_) {
-    const long long n = p.packed ? (long long)p.n_groups * p.H_kv * p.pre_tiles : 0;
+  __device__ Walk(const PagedParams& p_, const Start& s, bool pre, bool own) : p(p_) {
+    const long long n = pre ? (long long)p.n_groups * p.H_kv * p.pre_tiles : 0;
     const int parts = line_parts(p, n), c = blockIdx.x;
     pre_u = c < parts ? part_begin(n, parts, c) : 0;
     pre_end = c < parts ? part_begin(n, parts, c + 1) : 0;
-    own_left = s.left;
+    own_left = own ? s.left : 0;
     b = s.b;
     rc = s.rc;
     hk = s.hk;
-    tile = s.tile;
+    at = s.at;
     cur_b = -1;
     len = 0;
     own_first = (blockIdx.x & 1) != 0;
   }
   __device__ bool next(Seg& s) {
-    if (own_first && own_left > 0) return next_own(s);
+    if (own_first && own_left > 0) {
+      if (next_own(s)) return true;
+    }
     if (pre_u < pre_end) {
       const int item = (int)(pre_u / p.pre_tiles);
       s.own = false;
       s.hk = item / p.n_groups;
-      s.b = (item - s.hk * p.n_groups) * p.seqs * L::NWG;
+      s.b = (item - s.hk * p.n_groups) * p.seqs * (ITEM / 128);
       s.rc = 0;
       s.len = s.visible = 0;
       s.nt = p.pre_tiles;
       s.t0 = (int)(pre_u - (long long)item * p.pre_tiles);
       s.t1 = (int)min((long long)s.nt, s.t0 + (pre_end - pre_u));
-      s.pair = L::NWG == 2 && s.b + p.seqs < p.B;
-      s.steps = (s.t1 - s.t0) * (s.pair ? 2 : 1);
+      s.pair = ITEM == 256 && s.b + p.seqs < p.B;
       pre_u += s.t1 - s.t0;
       return true;
     }
     return own_left > 0 && next_own(s);
   }
   __device__ bool next_own(Seg& s) {
-    for (; b < p.B;) {
+    while (b < p.B && own_left > 0) {
       if (cur_b != b) {
         len = own_len(p, b);
         cur_b = b;
       }
-      const int vis = own_visible<128 * L::NWG>(p, len, rc);
-      const int nt = own_tiles<L::KT>(p, len, vis);
+      const int vis = own_visible<ITEM>(p, len, rc);
+      const int nt = own_tiles(p, len, vis);
+      int t0 = 0, t1 = 0;
       if (nt > 0) {
-        s.own = true;
-        s.b = b;
-        s.rc = rc;
-        s.hk = hk;
-        s.len = len;
-        s.visible = vis;
-        s.nt = nt;
-        s.t0 = tile;
-        s.t1 = (int)min((long long)nt, tile + own_left);
-        s.pair = L::NWG == 2 && p.R - rc * 256 > 128;
-        s.steps = (s.t1 - s.t0) * (s.pair ? 2 : 1);
-        own_left -= s.t1 - s.t0;
-        if (s.t1 < nt) {
-          tile = s.t1;
-          return true;
-        }
+        const int end = (int)min((long long)(nt + kItemCost), at + own_left);
+        t0 = max(0, at - kItemCost);
+        t1 = max(0, end - kItemCost);
+        own_left -= end - at;
       }
-      tile = 0;
-      // past this item; an item without tiles has none for the other heads either
+      at = 0;
+      s.rc = rc;
+      s.hk = hk;
+      s.b = b;
+      // past this item (a part that ends inside it has nothing left); an item without tiles has none
+      // for the other heads either
       if (nt == 0 || ++hk == p.H_kv) {
         hk = 0;
         if (++rc == p.n_rc) {
@@ -244,9 +334,18 @@ struct Walk {
           ++b;
         }
       }
-      if (nt > 0) return true;
+      if (t1 > t0) {
+        s.own = true;
+        s.len = len;
+        s.visible = vis;
+        s.nt = nt;
+        s.t0 = t0;
+        s.t1 = t1;
+        s.pair = ITEM == 256 && p.R - s.rc * 256 > 128;
+        return true;
+      }
     }
-    own_left = 0;  // the lengths changed under the call: stop instead of running past the batch
+    own_left = 0;
     return false;
   }
 };
@@ -256,28 +355,73 @@ struct TileInfo {
   bool pre;
   int k0, n;
 };
-template <int KT>
 __device__ __forceinline__ TileInfo tile_info(const PagedParams& p, const Seg& s, int t) {
   TileInfo x;
-  const int lead = s.own ? (p.packed ? 0 : p.pre_tiles) : p.pre_tiles;
+  const int lead = s.own && p.packed ? 0 : p.pre_tiles;
+  const int kt = s.own ? p.own_kt : p.pre_kt;
   x.pre = t < lead;
-  x.k0 = (x.pre ? t : t - lead) * KT;
-  x.n = min(KT, (x.pre ? p.prefix_len : s.visible) - x.k0);
+  x.k0 = (x.pre ? t : t - lead) << kt;
+  x.n = min(1 << kt, (x.pre ? p.prefix_len : s.visible) - x.k0);
   return x;
 }
 
-// ---------------------------------------------------------------------------- softmax step
-template <bool BF>
-__device__ __forceinline__ uint32_t pack16(float a, float b) {
-  return BF ? pack_bf16(a, b) : pack_f16(a, b);
+// Where a segment's results go.
+struct Place {
+  bool direct;        // the item is whole and nothing is to be joined
+  long long slot_row; // else: first row of the item's slot
+  int part;
+};
+template <int ITEM>
+__device__ __forceinline__ Place place_of(const PagedParams& p, const Seg& s) {
+  Place x;
+  const bool whole = s.t0 == 0 && s.t1 == s.nt;
+  x.direct = whole && s.own && (!p.packed || p.prefix_len == 0);
+  const long long item = s.own ? ((long long)s.b * p.n_rc + s.rc) * p.H_kv + s.hk
+                               : (long long)s.hk * p.n_groups + s.b / (p.seqs * (ITEM / 128));
+  const long long items = s.own ? (p.packed ? (long long)p.B * p.n_rc * p.H_kv : 0) : (long long)p.n_groups * p.H_kv;
+  x.part = s.own ? p.ctas - 1 - (int)blockIdx.x : (int)blockIdx.x;
+  const long long slot = whole ? item : items + 2 * x.part + (s.t0 == 0 ? 1 : 0);
+  x.slot_row = slot * (s.own ? min(p.R, ITEM) : ITEM);
+  return x;
+}
+// For the joining kernel: which parts of the own line hold the item (by the part that starts it).
+__device__ __forceinline__ void note_parts(const PagedParams& p, const Start& start, const Seg& s, int part) {
+  int last = part;
+  if (s.t1 < s.nt) {  // the item's last unit is nt - t1 units behind this part
+    const int parts = line_parts(p, start.total);
+    last = part_of(start.total, parts, part_begin(start.total, parts, part + 1) + (s.nt - s.t1) - 1);
+  }
+  p.seg[((long long)s.b * p.n_rc + s.rc) * p.H_kv + s.hk] = make_int2(part, last);
 }
 
+// The page of a tile's piece that starts at token `row0` of the tile.
+__device__ __forceinline__ int look_up(const PagedParams& p, const Seg& s, const TileInfo& x, int row0) {
+  const int none = max(p.num_pages, 1);  // one behind the last page: TMA reads zeros there
+  if (row0 >= x.n) return none;
+  const int e = (x.k0 + row0) >> p.page_shift;
+  const int page = x.pre ? p.prefix_table[e] : p.table[(long long)s.b * p.table_stride + e];
+  if (page >= 0 && page < p.num_pages) return page;
+  atomicExch(p.err, kDevIndex);
+  return none;
+}
+
+// Rows n .. of the keys of a V tile in shared memory set to zero (whole rows: the swizzle, which moves
+// 16-byte units inside a row, does not matter), by the 128 threads of a warpgroup.
+__device__ __forceinline__ void zero_rows(uint8_t* slot, int chunks, int chunk_bytes, int n) {
+  const int units = (chunk_bytes - n * 128) / 16;
+  for (int c = 0; c < chunks; ++c)
+    for (int z = (int)threadIdx.x & 127; z < units; z += 128)
+      *reinterpret_cast<uint4*>(slot + c * chunk_bytes + n * 128 + z * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------- dense form: softmax step
 // One step of a row: S from tensor memory, keys from `lim` on masked, running maximum, O rescaled
-// when the maximum has moved by 2^8 or more, P back over S.  `ready` waits until O may be touched.
+// when the maximum has moved by 2^8 or more, P back over S in parts of 64 keys (each announced on
+// its barrier, so that P V starts while the next part is computed).  `ready` waits until O may be touched.
 template <int D, bool BF, class Ready>
-__device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, float sl2, int lim, bool first, float& m,
-                                             float& l, Ready ready) {
-  constexpr int KT = PLayout<D>::KT;
+__device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, int lim, bool first, float& m, float& l,
+                                           uint32_t bar_p, Ready ready) {
+  constexpr int KT = Dense<D>::KT;
   float x[KT];
   {
     uint32_t u[KT / 32][32];
@@ -335,6 +479,9 @@ __device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, float sl2
       asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sb) : "l"(f2pack(e[2], e[3])));
     }
     tmem_st32(tS + 32 * h, pk);
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar_p + 8u * h);
   }
   float s0, s1, s2, s3;
   f2unpack(sa, s0, s1);
@@ -344,54 +491,715 @@ __device__ __forceinline__ bool softmax_step(uint32_t tS, uint32_t tO, float sl2
   return true;
 }
 
+// ---------------------------------------------------------------------------- dense form
+// Warps 0 - 3: copies and products.
+template <int D, bool BF>
+__device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedParams& p, const Start& start, bool pre,
+                                            bool own, uint32_t base, uint32_t bars, uint32_t tmem,
+                                           const WaitCtx& wctx) {
+  using L = Dense<D>;
+  constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
+  constexpr uint32_t NS = L::NS;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Walk<ITEM> walk(p, start, pre, own);
+  Seg sg;
+
+  if (warp == 0 || warp == 2) {
+    // ===================================================== page lookup and TMA: Q and K, or V
+    const int v = warp >> 1;
+    const CUtensorMap* map = v ? &maps.v : &maps.k;
+    const int per_chunk = KT / p.box_rows;  // boxes per column chunk of a tile
+    const int chunk = lane / per_chunk, row0 = (lane - chunk * per_chunk) * p.box_rows;
+    const bool has_box = chunk < L::KCH;
+    const int page_mask = (1 << p.page_shift) - 1;
+    uint32_t i = v, issued = 0;  // ring index of the next tile
+    int q_count[2] = {0, 0}, region = 0;
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      TileInfo x = tile_info(p, sg, sg.t0);
+      int page = has_box ? look_up(p, sg, x, row0) : 0;
+      if (v == 0) {
+        // Q: one region for a single tile (the other one keeps the previous item's), both for two tiles
+        for (int w = 0; w < (sg.pair ? 2 : 1); ++w) {
+          const int rg = sg.pair ? w : region;
+          if (q_count[rg] > 0 && !(ok = mbar_wait(bar(L::Q_EMPTY + rg), (q_count[rg] - 1) & 1, wctx))) break;
+          const int rows = min(p.R, 128) * (sg.own ? 1 : p.seqs);
+          if (lane == 0) mbar_arrive_expect_tx(bar(L::Q_FULL + rg), (uint32_t)rows * 128u * L::KCH);
+          __syncwarp();
+          if (lane < L::KCH)
+            tma_load_4d(base + rg * L::QTILE + lane * L::QCHUNK, sg.own ? &maps.q_own : &maps.q_pre, lane * 64,
+                        sg.own ? sg.rc * ITEM + w * 128 : 0, sg.hk, sg.own ? sg.b : sg.b + w * p.seqs,
+                        bar(L::Q_FULL + rg));
+          ++q_count[rg];
+        }
+        if (!ok) break;
+        if (NWG == 2 && !sg.pair) region ^= 1;
+      }
+      for (int t = sg.t0; t < sg.t1; ++t, i += 2) {
+        const TileInfo y = x;
+        const int cur = page;
+        if (t + 1 < sg.t1) {
+          x = tile_info(p, sg, t + 1);
+          if (has_box) page = look_up(p, sg, x, row0);
+        }
+        const uint32_t st = i % NS;
+        if (!(ok = mbar_wait(bar(L::KV_EMPTY + st), (i / NS & 1u) ^ 1u, wctx))) break;
+        const uint32_t boxes = (y.n + p.box_rows - 1) / p.box_rows;
+        if (lane == 0) mbar_arrive_expect_tx(bar(L::KV_FULL + st), boxes * p.box_rows * 128u * L::KCH);
+        __syncwarp();
+        if (has_box && row0 < y.n)
+          tma_load_4d(base + L::OFF_KV + st * L::SLOT + chunk * L::CHUNK + row0 * 128, map, chunk * 64,
+                      (y.k0 + row0) & page_mask, sg.hk, cur, bar(L::KV_FULL + st));
+        issued = i + 1;
+      }
+    }
+    // every copy asked for has landed before the phase ends (at once, unless a wait gave up)
+    for (uint32_t k = issued > NS ? issued - NS : 0; k < issued; ++k)
+      if ((k & 1u) == (uint32_t)v) drain_wait(bar(L::KV_FULL + k % NS), k / NS & 1u);
+    for (int rg = 0; rg < 2; ++rg)
+      if (q_count[rg] > 0) drain_wait(bar(L::Q_FULL + rg), (q_count[rg] - 1) & 1);
+  } else if (warp == 1) {
+    // ===================================================== products
+    const uint32_t leader = elect_one();
+    constexpr uint32_t idesc_qk = make_idesc(128, KT, BF, false, false);
+    constexpr uint32_t idesc_pv = make_idesc(128, D, BF, false, true);
+    const uint64_t dQ0 = make_sdesc_sw128(base, 16, 1024);
+    const uint64_t dK0 = make_sdesc_sw128(base + L::OFF_KV, 16, 1024);
+    const uint64_t dV0 = make_sdesc_sw128(base + L::OFF_KV, L::CHUNK, 1024);
+    bool ok = true;
+    // what the P V of a step has to know, kept from its S, two steps earlier
+    struct Step {
+      bool valid, first, last_use, ends;
+      uint32_t i;  // ring index of the V tile
+    };
+    int n_steps = 0, s = 0, region = 0, q_use[2] = {0, 0};
+    uint32_t seg_i = 0, s_total = 0;  // ring index of the segment's first K tile; steps so far
+    bool more = true, have = false;
+    auto issue_s = [&]() -> Step {
+      Step f{};
+      if (!more) return f;
+      if (s == n_steps) {
+        if (have) {
+          seg_i += 2 * (sg.t1 - sg.t0);
+          if (NWG == 2 && !sg.pair) region ^= 1;
+        }
+        if (!(more = walk.next(sg))) return f;
+        have = true;
+        s = 0;
+        n_steps = (sg.t1 - sg.t0) << (sg.pair ? 1 : 0);
+      }
+      const int q = sg.pair ? (s & 1) : 0;  // query tile
+      const int rg = sg.pair ? q : region, per = sg.pair ? 2 : 1;
+      const uint32_t i = seg_i + 2u * (uint32_t)(sg.pair ? s >> 1 : s), st = i % NS, sb = s_total & 1u;
+      if (s < per) {
+        if (!(ok = mbar_wait(bar(L::Q_FULL + rg), q_use[rg] & 1, wctx))) return f;
+        ++q_use[rg];
+      }
+      if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) return f;
+      tc_fence_after();
+      const uint64_t dq = sdesc_add(dQ0, rg * L::QTILE), dk = sdesc_add(dK0, st * L::SLOT);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(tmem + L::T_S(sb), sdesc_add(dq, (k / 4) * L::QCHUNK + (k % 4) * 32),
+               sdesc_add(dk, (k / 4) * L::CHUNK + (k % 4) * 32), idesc_qk, k > 0 ? 1u : 0u, leader);
+      mma_commit(bar(L::S_FULL + sb), leader);
+      if (q == per - 1) mma_commit(bar(L::KV_EMPTY + st), leader);
+      if (s >= n_steps - per) mma_commit(bar(L::Q_EMPTY + rg), leader);
+      f.valid = true;
+      f.first = s < NWG;  // this accumulator's first product of the segment
+      f.last_use = q == per - 1;
+      f.ends = s >= n_steps - per;
+      f.i = i + 1;
+      ++s;
+      ++s_total;
+      return f;
+    };
+    Step f0 = issue_s();
+    Step f1{};
+    if (ok) f1 = issue_s();
+    int o_use[2] = {0, 0};
+    for (uint32_t total = 0; ok && f0.valid; ++total) {
+      const uint32_t sb = total & 1u, w = NWG == 2 ? sb : 0, st = f0.i % NS;
+      if (f0.first) {  // the accumulator's last results have been read
+        if (o_use[w] > 0 && !(ok = mbar_wait(bar(L::O_FREE + w), (o_use[w] - 1) & 1, wctx))) break;
+        ++o_use[w];
+      }
+      if (!(ok = mbar_wait(bar(L::KV_FULL + st), f0.i / NS & 1u, wctx))) break;
+      const uint64_t dv = sdesc_add(dV0, st * L::SLOT);
+#pragma unroll
+      for (int h = 0; h < L::HALVES; ++h) {
+        if (!(ok = mbar_wait(bar(L::P_FULL + 2 * sb + h), total / 2 & 1u, wctx))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 4 * h; k < 4 * h + 4; ++k)
+          mma_ts(tmem + L::T_O(w), tmem + L::T_S(sb) + k * 8, sdesc_add(dv, k * 2048), idesc_pv,
+                 (!f0.first || k > 0) ? 1u : 0u, leader);
+      }
+      if (!ok) break;
+      if (f0.last_use) mma_commit(bar(L::KV_EMPTY + st), leader);
+      if (NWG == 1) mma_commit(bar(L::PV_DONE), leader);
+      if (f0.ends) mma_commit(bar(L::O_FULL + w), leader);
+      f0 = f1;
+      f1 = issue_s();
+    }
+    mma_commit(bar(L::MMA_DONE), leader);
+    drain_wait(bar(L::MMA_DONE), 0);
+  }
+}
+
+// Warps 4 - 11: softmax.
+template <int D, bool BF>
+__device__ __forceinline__ void dense_softmax(const PagedParams& p, const Start& start, bool pre, bool own,
+                                              uint8_t* gbase, uint32_t bars, uint32_t tmem, const WaitCtx& wctx) {
+  using L = Dense<D>;
+  constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
+  constexpr uint32_t NS = L::NS;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = (warp - 4) >> 2;
+  if (w < NWG) {
+    Walk<ITEM> walk(p, start, pre, own);
+    Seg sg;
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+    float2* stat = reinterpret_cast<float2*>(gbase + L::OFF_STAT);
+    bool ok = true;
+    uint32_t kv = 0, total = 0;  // key tiles and steps of earlier segments
+    int o_cnt = 0;               // segments that this warpgroup ended
+    int stat_cnt = 0;            // statistics handed over (by either warpgroup)
+    while (ok && walk.next(sg)) {
+      const int steps = (sg.t1 - sg.t0) << (sg.pair ? 1 : 0);
+      const int s_first = NWG == 2 ? (w ^ (int)(total & 1u)) : 0;
+      const int tile_q = sg.pair ? s_first : 0;  // this warpgroup's query tile
+      // rows of the tile
+      const int live = sg.own ? min(128, p.R - sg.rc * ITEM - tile_q * 128)
+                              : min(p.seqs, p.B - sg.b - tile_q * p.seqs) * p.R;
+      const bool warp_live = wq * 32 < live;
+      bool counts = row < live;  // rows of a sequence that is not there may hold anything
+      if (counts && !sg.own) counts = p.lens[sg.b + tile_q * p.seqs + row / p.R] >= 0;
+      int own_lim = sg.visible;
+      if (sg.own && p.causal) own_lim = sg.len - p.T + (sg.rc * ITEM + tile_q * 128 + row) % p.T + 1;
+      float m = -INFINITY, l = 0.f;
+      bool mine = false;
+      for (int s = s_first; s < steps; s += NWG) {
+        const uint32_t n = total + s, sb = n & 1u;
+        const int kt = sg.pair ? s >> 1 : s;
+        const TileInfo x = tile_info(p, sg, sg.t0 + kt);
+        if (x.n < KT && (!sg.pair || s_first == 0)) {
+          // the tile ends behind the last token: rows x.n .. of V are whatever was there before
+          const uint32_t i = 2 * (kv + kt) + 1, st = i % NS;
+          if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) break;
+          zero_rows(gbase + L::OFF_KV + st * L::SLOT, L::KCH, L::CHUNK, x.n);
+          fence_proxy_async_smem();
+        }
+        if (!(ok = mbar_wait(bar(L::S_FULL + sb), n / 2 & 1u, wctx))) break;
+        tc_fence_after();
+        const uint32_t bar_p = bar(L::P_FULL + 2 * sb);
+        if (warp_live) {
+          const int lim = x.pre ? x.n : min(x.n, own_lim - x.k0);
+          ok = dense_step<D, BF>(tmem + lanes + L::T_S(sb), tmem + lanes + L::T_O(w), p.scale_log2, lim, !mine, m, l,
+                                 bar_p, [&]() -> bool {
+                                   // one accumulator: the previous step's product may still run
+                                   if constexpr (NWG == 1) return mbar_wait(bar(L::PV_DONE), (n - 1) & 1u, wctx);
+                                   return true;
+                                 });
+          if (!ok) break;
+          // weights are at most 2^8: a sum that is no finite number came from a non-finite score
+          // (a wrong page may be the reason, and that report stays)
+          if (counts && !(l <= 3.0e38f)) atomicCAS(p.err, kDevOk, kDevRange);
+        } else {
+          for (int h = 0; h < L::HALVES; ++h) mbar_arrive(bar_p + 8u * h);
+        }
+        mine = true;
+      }
+      total += steps;
+      kv += sg.t1 - sg.t0;
+      if (!ok) break;
+      if (!mine) continue;
+      // ---- the end of a segment.  Two tiles: each warpgroup has its own rows.  One tile: the
+      // warpgroup of the last step joins the other's m, l (through shared memory) and O.
+      const bool other = NWG == 2 && !sg.pair && steps > 1;
+      float2 theirs = make_float2(-INFINITY, 0.f);
+      if (other) {
+        if (((total - 1) & 1u) != (uint32_t)w) {
+          if (stat_cnt > 0 && !(ok = mbar_wait(bar(L::STAT_EMPTY), (stat_cnt - 1) & 1, wctx))) break;
+          stat[row] = make_float2(m, l);
+          mbar_arrive(bar(L::STAT_FULL));
+          ++stat_cnt;
+          continue;
+        }
+        if (!(ok = mbar_wait(bar(L::STAT_FULL), stat_cnt & 1, wctx))) break;
+        ++stat_cnt;
+        theirs = stat[row];
+        mbar_arrive(bar(L::STAT_EMPTY));
+      }
+      if (!(ok = mbar_wait(bar(L::O_FULL + w), o_cnt & 1, wctx))) break;
+      ++o_cnt;
+      tc_fence_after();
+      const float M = fmaxf(m, theirs.x);
+      float ca = M == -INFINITY ? 0.f : ex2_approx(m - M);
+      float cb = M == -INFINITY ? 0.f : ex2_approx(theirs.x - M);
+      const float sum = ca * l + cb * theirs.y;
+      const Place pl = place_of<ITEM>(p, sg);
+      if (sg.own && sg.t0 == 0 && tile_q == 0 && row == 0) note_parts(p, start, sg, pl.part);
+      if (pl.direct) {
+        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        ca *= inv;
+        cb *= inv;
+      }
+      const bool write = row < live;
+      const long long out_row = ((long long)sg.b * p.H_kv + sg.hk) * p.R + sg.rc * ITEM + tile_q * 128 + row;
+      const long long srow = pl.slot_row + tile_q * 128 + row;
+      const uint32_t tO = tmem + lanes + L::T_O(w), tO2 = tmem + lanes + L::T_O(w ^ 1);
+      uint8_t* dst = pl.direct ? static_cast<uint8_t*>(p.o) + out_row * (2 * D)
+                               : reinterpret_cast<uint8_t*>((sg.own ? p.own_o : p.pre_o) + srow * D);
+      if (warp_live) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          tmem_ld32(tO + 32 * c, u);
+          if (other) {
+            uint32_t v[32];
+            tmem_ld32(tO2 + 32 * c, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              u[i] = __float_as_uint(fmaf(ca, __uint_as_float(u[i]), cb * __uint_as_float(v[i])));
+          } else {
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(ca * __uint_as_float(u[i]));
+          }
+          if (write && pl.direct) {
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              h[i] = pack16<BF>(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(dst + c * 64 + i * 16) =
+                  make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+          } else if (write) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_global_32b(dst + c * 128 + i * 32, u + 8 * i);
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(L::O_FREE + w));
+      if (other) mbar_arrive(bar(L::O_FREE + (w ^ 1)));
+      if (write) {
+        if (!pl.direct)
+          (sg.own ? p.own_ml : p.pre_ml)[srow] = make_float2(M, sum);
+        else if (p.lse != nullptr)
+          p.lse[out_row] = log_sum(M, sum);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- few rows: softmax
+// Sums of v[r] over the 32 lanes for all r at once: halves of the rows go to halves of the lanes, so
+// N values cost N - 1 exchanges (and log2(32 / N) more); lane l ends with the sum of row l % N.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+  if constexpr (N > 1) {
+    constexpr int H = N / 2;
+    const bool up = (lane & H) != 0;
+    float w[H];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const float send = up ? v[i] : v[i + H], keep = up ? v[i + H] : v[i];
+      w[i] = keep + __shfl_xor_sync(0xffffffffu, send, H);
+    }
+    return warp_sums<H>(w, lane);
+  } else {
+    return v[0];
+  }
+}
+
+// A warpgroup's work on one segment with up to N rows (N = 8, 16 or 32): thread k has key k of
+// every tile and, in the end, column k of O.
+template <int D, bool BF, int N>
+__device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& start, const Seg& sg, uint32_t bars,
+                                            uint8_t* gbase, uint32_t tmem, const WaitCtx& wctx, int w, uint32_t kv,
+                                            uint32_t seg_no) {
+  using L = Few<D>;
+  constexpr uint32_t NS = L::NS;
+  constexpr int ITEM = 128 * Dense<D>::NWG;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
+  const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, key = wq * 32 + lane;
+  const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+  const int rows = sg.own ? p.R : p.R * p.B;
+  const int id = 1 + w;
+  float4* ex = reinterpret_cast<float4*>(gbase + L::OFF_EX) + w * 64;  // [2][32]: a value of each warp per row
+  uint32_t ex_no = 0;
+  float m[N], l[N];
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+  }
+  const int n_tiles = sg.t1 - sg.t0;
+  for (int t = 0; t < n_tiles; ++t) {
+    const uint32_t n = kv + t;  // step of the phase
+    const TileInfo x = tile_info(p, sg, sg.t0 + t);
+    if (!mbar_wait(bar(L::S_FULL + (n & 3u)), n / 4 & 1u, wctx)) return false;
+    tc_fence_after();
+    float s[N];
+    {
+      uint32_t u[N];
+      tmem_ld<N>(tmem + lanes + L::T_S(n & 3u), u);
+      tmem_wait_ld();
+#pragma unroll
+      for (int r = 0; r < N; ++r) s[r] = __uint_as_float(u[r]) * p.scale_log2;
+    }
+    // masks: rows that are not there, and keys that a row does not see.  All rows of a prefix
+    // tile, and all of a sequence's with one token each, see the same keys.
+    const bool steps_in = !x.pre && p.causal && p.T > 1;  // rows differ
+    const int first_lim = steps_in ? sg.len - p.T + 1 - x.k0 : x.n;
+    if (rows < N || first_lim < 128) {
+      int tok = 0;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        if (r >= rows || key >= min(x.n, first_lim + tok)) s[r] = -INFINITY;
+        if (steps_in && ++tok == p.T) tok = 0;
+      }
+    }
+    bool above = false;
+#pragma unroll
+    for (int r = 0; r < N; ++r) above |= s[r] > m[r] + 8.0f;
+    if (group_any(id, above)) {
+      // a maximum has moved by 2^8 or more (always on the first tile): take the tile's maxima
+      float mine = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float t_max = warp_max(s[r]);
+        if (lane == r) mine = t_max;
+      }
+      float4* e = ex + (ex_no++ & 1u) * 32;
+      if (lane < N) reinterpret_cast<float*>(e + lane)[wq] = mine;
+      group_sync(id);
+      float alpha[N];
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float4 v = e[r];
+        const float m_new = fmaxf(m[r], fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+        const float m_use = (m_new - m[r] > 8.0f) ? m_new : m[r];
+        alpha[r] = m_use == m[r] ? 1.0f : ex2_approx(m[r] - m_use);
+        moved |= alpha[r] != 1.0f;
+        m[r] = m_use;
+        l[r] *= alpha[r];
+      }
+      if (moved && t > 0) {  // (the same for all threads)
+        // O^T holds the earlier tiles once their products have completed
+        if (!mbar_wait(bar(L::P_EMPTY + ((n - 1) & 1u)), (n - 1) / 2 & 1u, wctx)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < L::PARTS; ++h) {
+          uint32_t u[N];
+          tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < N; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * alpha[r]);
+          tmem_st<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u);
+        }
+        tmem_wait_st();
+      }
+    }
+    // P^T: row r of the buffer holds the weights of query row r, 64 keys to a 128-byte row of a chunk
+    if (n >= 2 && !mbar_wait(bar(L::P_EMPTY + (n & 1u)), (n / 2 - 1) & 1u, wctx)) return false;
+    uint8_t* pb = gbase + L::OFF_P + (n & 1u) * 2 * L::RCHUNK + (key >> 6) * L::RCHUNK + (key & 7) * 2;
+    const uint32_t unit = (uint32_t)(key & 63) >> 3;
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const float e = ex2_approx(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+      l[r] += e;
+      *reinterpret_cast<uint16_t*>(pb + r * 128 + ((unit ^ (r & 7)) << 4)) = round16<BF>(e);
+    }
+    if (x.n < 128) {
+      // the tile ends behind the last token: rows x.n .. of V are whatever was there before
+#pragma unroll
+      for (int h = 0; h < L::PARTS; ++h) {
+        const uint32_t i = (2 * n + 1) * L::PARTS + h, st = i % NS;
+        if (!mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx)) return false;
+        zero_rows(gbase + st * L::SLOT, L::PCH, L::CHUNK, x.n);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    mbar_arrive(bar(L::P_FULL + (n & 1u)));
+  }
+  // ---- the end of the segment: row sums over the threads, then column `key` of each row
+  float total[N];
+  {
+    float v = warp_sums<N>(l, lane);
+#pragma unroll
+    for (int d = N; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    float4* e = ex + (ex_no++ & 1u) * 32;
+    if (lane < N) reinterpret_cast<float*>(e + lane)[wq] = v;
+    group_sync(id);
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const float4 q = e[r];
+      total[r] = (q.x + q.y) + (q.z + q.w);
+    }
+  }
+  const Place pl = place_of<ITEM>(p, sg);
+  if (sg.own && sg.t0 == 0 && key == 0) note_parts(p, start, sg, pl.part);
+  const long long out_row = ((long long)sg.b * p.H_kv + sg.hk) * p.R;  // own items
+#pragma unroll
+  for (int r = 0; r < N; ++r)
+    if (key == r && r < rows) {
+      if (!(total[r] <= 3.0e38f) && (sg.own || p.lens[r / p.R] >= 0)) atomicCAS(p.err, kDevOk, kDevRange);
+      if (!pl.direct)
+        (sg.own ? p.own_ml : p.pre_ml)[pl.slot_row + r] = make_float2(m[r], total[r]);
+      else if (p.lse != nullptr)
+        p.lse[out_row + r] = log_sum(m[r], total[r]);
+    }
+  if (!mbar_wait(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx)) return false;
+  tc_fence_after();
+  uint32_t u[L::PARTS][N];
+#pragma unroll
+  for (int h = 0; h < L::PARTS; ++h) tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u[h]);
+  tmem_wait_ld();
+  tc_fence_before();
+  mbar_arrive(bar(L::O_FREE + (seg_no & 1u)));
+  if (D >= 128 || key < D) {
+#pragma unroll
+    for (int h = 0; h < L::PARTS; ++h)
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        if (r >= rows) continue;
+        const float v = __uint_as_float(u[h][r]);
+        const int col = h * 128 + key;
+        if (pl.direct)
+          static_cast<uint16_t*>(p.o)[(out_row + r) * D + col] =
+              round16<BF>(total[r] > 0.f ? v * __frcp_rn(total[r]) : 0.f);
+        else
+          (sg.own ? p.own_o : p.pre_o)[(pl.slot_row + r) * D + col] = v;
+      }
+  }
+  return true;
+}
+
+// Warps 0 - 3: copies and products.
+template <int D, bool BF>
+__device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParams& p, const Start& start, bool pre,
+                                          bool own, uint32_t base, uint32_t bars, uint32_t tmem,
+                                         const WaitCtx& wctx) {
+  using L = Few<D>;
+  constexpr uint32_t NS = L::NS, NQ = L::NQ;
+  constexpr int PARTS = L::PARTS, ITEM = 128 * Dense<D>::NWG;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Walk<ITEM> walk(p, start, pre, own);
+  Seg sg;
+
+  if (warp == 0 || warp == 2) {
+    // ===================================================== page lookup and TMA: Q and K, or V
+    const int v = warp >> 1;
+    const CUtensorMap* map = v ? &maps.v : &maps.k;
+    const int per_chunk = 128 / p.box_rows;
+    const int chunk = lane / per_chunk, row0 = (lane - chunk * per_chunk) * p.box_rows;
+    const bool has_box = chunk < L::PCH;
+    const int page_mask = (1 << p.page_shift) - 1;
+    uint32_t i = v * PARTS, seg_no = 0;  // ring index of the next tile
+    uint32_t issued = 0;                 // ring index behind the last slot asked for
+    bool ok = true;
+    for (; ok && walk.next(sg); ++seg_no) {
+      TileInfo x = tile_info(p, sg, sg.t0);
+      int page = has_box ? look_up(p, sg, x, row0) : 0;
+      if (v == 0) {
+        const uint32_t qb = seg_no % NQ;
+        if (seg_no >= NQ && !(ok = mbar_wait(bar(L::Q_EMPTY + qb), (seg_no / NQ - 1) & 1u, wctx))) break;
+        const int rows = sg.own ? p.R : p.R * p.B;
+        if (lane == 0) mbar_arrive_expect_tx(bar(L::Q_FULL + qb), (uint32_t)rows * 128u * L::KCH);
+        __syncwarp();
+        if (lane < L::KCH)
+          tma_load_4d(base + L::OFF_Q + (qb * L::KCH + lane) * L::RCHUNK, sg.own ? &maps.q_own : &maps.q_pre, lane * 64,
+                      0, sg.hk, sg.own ? sg.b : 0, bar(L::Q_FULL + qb));
+      }
+      for (int t = sg.t0; t < sg.t1 && ok; ++t, i += 2 * PARTS) {
+        const TileInfo y = x;
+        const int cur = page;
+        if (t + 1 < sg.t1) {
+          x = tile_info(p, sg, t + 1);
+          if (has_box) page = look_up(p, sg, x, row0);
+        }
+        const uint32_t bytes = (uint32_t)((y.n + p.box_rows - 1) / p.box_rows) * p.box_rows * 128u * L::PCH;
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) {
+          const uint32_t st = (i + h) % NS;
+          if (!(ok = mbar_wait(bar(L::KV_EMPTY + st), ((i + h) / NS & 1u) ^ 1u, wctx))) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(L::KV_FULL + st), bytes);
+          __syncwarp();
+          if (has_box && row0 < y.n)
+            tma_load_4d(base + st * L::SLOT + chunk * L::CHUNK + row0 * 128, map, (h * L::PCH + chunk) * 64,
+                        (y.k0 + row0) & page_mask, sg.hk, cur, bar(L::KV_FULL + st));
+          issued = i + h + 1;
+        }
+      }
+    }
+    // every copy asked for has landed before the phase ends (at once, unless a wait gave up)
+    for (uint32_t k = issued > NS ? issued - NS : 0; k < issued; ++k)
+      if ((k / PARTS & 1u) == (uint32_t)v) drain_wait(bar(L::KV_FULL + k % NS), k / NS & 1u);
+    if (v == 0)
+      for (uint32_t k = seg_no > NQ ? seg_no - NQ : 0; k < seg_no; ++k)
+        drain_wait(bar(L::Q_FULL + k % NQ), k / NQ & 1u);
+  } else if (warp == 1) {
+    // ===================================================== products
+    const uint32_t leader = elect_one();
+    constexpr uint32_t idesc_s = make_idesc(128, 0, BF, false, false);  // + columns: 16 or 32
+    constexpr uint32_t idesc_o = make_idesc(128, 0, BF, true, false);
+    const uint64_t dK0 = make_sdesc_sw128(base, 16, 1024);
+    const uint64_t dV0 = make_sdesc_sw128(base, L::CHUNK, 1024);
+    const uint64_t dQ0 = make_sdesc_sw128(base + L::OFF_Q, 16, 1024);
+    const uint64_t dP0 = make_sdesc_sw128(base + L::OFF_P, 16, 1024);
+    bool ok = true;
+    struct Step {
+      bool valid, first, last;
+      uint32_t seg_no, cols;
+    };
+    int t = 0, n_tiles = 0;
+    uint32_t n_s = 0, seg_no = 0xffffffffu, cols = 0;
+    bool more = true;
+    auto issue_s = [&]() -> Step {
+      Step f{};
+      if (!more) return f;
+      if (t == n_tiles) {
+        if (!(more = walk.next(sg))) return f;
+        ++seg_no;
+        t = 0;
+        n_tiles = sg.t1 - sg.t0;
+        cols = (sg.own ? p.R : p.R * p.B) <= 16 ? 16 : 32;
+      }
+      const uint32_t qb = seg_no % NQ;
+      if (t == 0 && !(ok = mbar_wait(bar(L::Q_FULL + qb), seg_no / NQ & 1u, wctx))) return f;
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        const uint32_t i = 2 * n_s * PARTS + h, st = i % NS;
+        if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) return f;
+        tc_fence_after();
+        const uint64_t dk = sdesc_add(dK0, st * L::SLOT);
+        const uint64_t dq = sdesc_add(dQ0, (qb * L::KCH + h * L::PCH) * L::RCHUNK);
+#pragma unroll
+        for (int k = 0; k < 4 * L::PCH; ++k)
+          mma_ss(tmem + L::T_S(n_s & 3u), sdesc_add(dk, (k / 4) * L::CHUNK + (k % 4) * 32),
+                 sdesc_add(dq, (k / 4) * L::RCHUNK + (k % 4) * 32), idesc_s | (cols >> 3) << 17,
+                 (h > 0 || k > 0) ? 1u : 0u, leader);
+        mma_commit(bar(L::KV_EMPTY + st), leader);
+      }
+      mma_commit(bar(L::S_FULL + (n_s & 3u)), leader);
+      if (t == n_tiles - 1) mma_commit(bar(L::Q_EMPTY + qb), leader);
+      f.valid = true;
+      f.first = t == 0;
+      f.last = t == n_tiles - 1;
+      f.seg_no = seg_no;
+      f.cols = cols;
+      ++t;
+      ++n_s;
+      return f;
+    };
+    Step f0 = issue_s();
+    Step f1{};
+    if (ok) f1 = issue_s();
+    for (uint32_t n = 0; ok && f0.valid; ++n) {
+      const uint32_t par = f0.seg_no & 1u;
+      if (f0.first && f0.seg_no >= 2 && !(ok = mbar_wait(bar(L::O_FREE + par), (f0.seg_no / 2 - 1) & 1u, wctx))) break;
+      if (!(ok = mbar_wait(bar(L::P_FULL + (n & 1u)), n / 2 & 1u, wctx))) break;
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h) {
+        const uint32_t i = (2 * n + 1) * PARTS + h, st = i % NS;
+        if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) break;
+        tc_fence_after();
+        const uint64_t dv = sdesc_add(dV0, st * L::SLOT), dp = sdesc_add(dP0, (n & 1u) * 2 * L::RCHUNK);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ss(tmem + L::T_O(par, h), sdesc_add(dv, k * 2048), sdesc_add(dp, (k / 4) * L::RCHUNK + (k % 4) * 32),
+                 idesc_o | (f0.cols >> 3) << 17, (!f0.first || k > 0) ? 1u : 0u, leader);
+        mma_commit(bar(L::KV_EMPTY + st), leader);
+      }
+      if (!ok) break;
+      mma_commit(bar(L::P_EMPTY + (n & 1u)), leader);
+      if (f0.last) mma_commit(bar(L::O_FULL + par), leader);
+      f0 = f1;
+      f1 = issue_s();
+    }
+    mma_commit(bar(L::MMA_DONE), leader);
+    drain_wait(bar(L::MMA_DONE), 0);
+  }
+}
+
+// Warps 4 - 11: softmax, the two warpgroups take segments in turn.
+template <int D, bool BF>
+__device__ __forceinline__ void few_softmax(const PagedParams& p, const Start& start, bool pre, bool own, uint8_t* gbase,
+                                            uint32_t bars, uint32_t tmem, const WaitCtx& wctx) {
+  Walk<128 * Dense<D>::NWG> walk(p, start, pre, own);
+  Seg sg;
+  const int w = (int)(threadIdx.x >> 7) - 1;
+  uint32_t kv = 0, seg_no = 0;
+  for (; walk.next(sg); kv += sg.t1 - sg.t0, ++seg_no) {
+    if ((seg_no & 1u) != (uint32_t)w) continue;
+    const int rows = sg.own ? p.R : p.R * p.B;
+    const bool ok = rows <= 8    ? few_segment<D, BF, 8>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no)
+                    : rows <= 16 ? few_segment<D, BF, 16>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no)
+                                 : few_segment<D, BF, 32>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no);
+    if (!ok) break;
+  }
+}
+
 // ---------------------------------------------------------------------------- attention
 template <int D, bool BF>
-__global__ void __launch_bounds__(PLayout<D>::THREADS, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     fa_paged_attn_sm100_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedParams p) {
-  using L = PLayout<D>;
-  constexpr int KT = L::KT, NWG = L::NWG, NS = L::NS, ITEM = 128 * NWG;
+  using M = Smem<D>;
+  constexpr int ITEM = 128 * Dense<D>::NWG;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  auto bar = [&](int i) -> uint32_t { return base + L::OFF_BAR + 8u * i; };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::OFF_ABORT);
+  const uint32_t bars = base + M::OFF_BAR;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + M::OFF_ABORT);
   const WaitCtx wctx{abort_flag, p.err};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Start& start = *reinterpret_cast<Start*>(gbase + L::OFF_START);
+  Start& start = *reinterpret_cast<Start*>(gbase + M::OFF_START);
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(L::BAR_Q_FULL + i), 1);
-      mbar_init(bar(L::BAR_Q_EMPTY + i), 1);
-      mbar_init(bar(L::BAR_S_FULL + i), 1);
-      mbar_init(bar(L::BAR_P_FULL + i), 128);
-      mbar_init(bar(L::BAR_O_FULL + i), 1);
-      mbar_init(bar(L::BAR_O_FREE + i), 128);
-    }
-    mbar_init(bar(L::BAR_STAT_FULL), 128);
-    mbar_init(bar(L::BAR_STAT_EMPTY), 128);
-    mbar_init(bar(L::BAR_PV_DONE), 1);
-    mbar_init(bar(L::BAR_MMA_DONE), 1);
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(bar(L::BAR_KV_FULL + i), 1);
-      mbar_init(bar(L::BAR_KV_EMPTY + i), 1);
-    }
+  if (threadIdx.x < Dense<D>::NBAR + Few<D>::NBAR) {
+    // arrivals: the 128 threads of a warpgroup where P, O or statistics are handed over, else 1
+    const int i = threadIdx.x, f = i - Dense<D>::NBAR;
+    using A = Dense<D>;
+    using F = Few<D>;
+    const bool group = f < 0 ? (i >= A::P_FULL && i < A::P_FULL + 4) || (i >= A::O_FREE && i < A::O_FREE + 2) ||
+                                   i == A::STAT_FULL || i == A::STAT_EMPTY
+                             : (f >= F::P_FULL && f < F::P_FULL + 2) || (f >= F::O_FREE && f < F::O_FREE + 2);
+    mbar_init(bars + 8u * i, group ? 128 : 1);
     fence_barrier_init();
   }
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    start.left = 0;
+  }
   if (warp == 1) {
-    tmem_alloc(base + L::OFF_TMEM_SLOT, 512);
+    tmem_alloc(base + M::OFF_TMEM_SLOT, 512);
     tmem_relinquish();
   }
   // ---- this CTA's part of the own line: every thread adds up the units of its share of the
   // sequences, the block scans the sums, and the thread whose share holds the part's first unit finds it
   {
-    long long* scan = reinterpret_cast<long long*>(gbase + L::OFF_SCAN);
-    const int per = (int)ceil_div(p.B, L::THREADS);
+    long long* scan = reinterpret_cast<long long*>(gbase + M::OFF_SCAN);
+    const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units_of<D>(p, b);
+    for (int b = b0; b < b1; ++b) {
+      mine += units_of<ITEM>(p, b);
+      if (blockIdx.x == 0 && p.lens[b] > ((long long)p.max_pages << p.page_shift))
+        atomicExch(p.err, kDevIndex);  // a length that the table cannot hold
+    }
     long long x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -399,11 +1207,10 @@ __global__ void __launch_bounds__(PLayout<D>::THREADS, 1)
       if (lane >= d) x += y;
     }
     if (lane == 31) scan[warp] = x;
-    if (threadIdx.x == 0) start.left = 0;
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < L::THREADS / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += scan[w];
       total += scan[w];
     }
@@ -413,383 +1220,71 @@ __global__ void __launch_bounds__(PLayout<D>::THREADS, 1)
     const long long hi = part < parts ? part_begin(total, parts, part + 1) : 0;
     if (hi > lo && before <= lo && lo < before + mine) {
       long long skip = lo - before;
-      for (int b = b0; b < b1; ++b) {
-        const long long n = units_of<D>(p, b);
-        if (skip >= n) {
-          skip -= n;
+      int b = b0;
+      for (long long n; b < b1 && skip >= (n = units_of<ITEM>(p, b)); ++b) skip -= n;
+      const int len = own_len(p, b);
+      for (int rc = 0; rc < p.n_rc; ++rc) {
+        const int n = item_units(own_tiles(p, len, own_visible<ITEM>(p, len, rc)));
+        if (skip >= (long long)n * p.H_kv) {
+          skip -= (long long)n * p.H_kv;
           continue;
         }
-        const int len = own_len(p, b);
-        for (int rc = 0; rc < p.n_rc; ++rc) {
-          const int nt = own_tiles<KT>(p, len, own_visible<ITEM>(p, len, rc));
-          if (skip >= (long long)nt * p.H_kv) {
-            skip -= (long long)nt * p.H_kv;
-            continue;
-          }
-          start.b = b;
-          start.rc = rc;
-          start.hk = (int)(skip / nt);
-          start.tile = (int)(skip - (long long)start.hk * nt);
-          start.left = hi - lo;
-          break;
-        }
+        start.b = b;
+        start.rc = rc;
+        start.hk = (int)(skip / n);
+        start.at = (int)(skip - (long long)start.hk * n);
+        start.left = hi - lo;
         break;
       }
     }
     if (threadIdx.x == 0) start.total = total;
-    if (blockIdx.x == 0)  // lengths that the table cannot hold
-      for (int b = b0; b < b1; ++b)
-        if (p.lens[b] > ((long long)p.max_pages << p.page_shift)) atomicExch(p.err, kDevIndex);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + L::OFF_TMEM_SLOT);
-  Walk<D> walk(p, start);
-  Seg sg;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + M::OFF_TMEM_SLOT);
 
-  if (warp == 0) {
-    // ===================================================== page lookup and TMA
-    if constexpr (NWG == 2) regs_dec<kRegsLow>();
-    const int per_chunk = KT / p.box_rows;      // boxes per column chunk of a tile
-    const int chunk = lane / per_chunk, piece = lane - chunk * per_chunk;
-    const bool has_box = chunk < L::KCH;
-    const int row0 = piece * p.box_rows;        // first token of this lane's box inside the tile
-    const uint32_t box_bytes = (uint32_t)p.box_rows * 128u;
-    const int page_mask = (1 << p.page_shift) - 1;
-    const int no_page = max(p.num_pages, 1);    // reads zeros
-    long long kv = 0, issued = 0;  // key tiles and ring slots filled so far
-    int q_count[2] = {0, 0}, region = 0;
-    bool ok = true;
-    // the page of this lane's box in tile t
-    auto look_up = [&](const Seg& s, int t) -> int {
-      const TileInfo x = tile_info<KT>(p, s, t);
-      if (!has_box || row0 >= x.n) return no_page;
-      const int e = (x.k0 + row0) >> p.page_shift;
-      const int page = x.pre ? p.prefix_table[e] : p.table[(long long)s.b * p.table_stride + e];
-      if (page >= 0 && page < p.num_pages) return page;
-      atomicExch(p.err, kDevIndex);
-      return no_page;
-    };
-    while (ok && walk.next(sg)) {
-      int page = look_up(sg, sg.t0);
-      // Q: one region for a single tile (the other one keeps the previous item's), both for two tiles
-      for (int w = 0; w < (sg.pair ? 2 : 1) && ok; ++w) {
-        const int rg = sg.pair ? w : region;
-        if (q_count[rg] > 0 && !(ok = mbar_wait(bar(L::BAR_Q_EMPTY + rg), (q_count[rg] - 1) & 1, wctx))) break;
-        const int rows = min(p.R, 128) * (sg.own ? 1 : p.seqs);
-        if (lane == 0) mbar_arrive_expect_tx(bar(L::BAR_Q_FULL + rg), (uint32_t)rows * 128u * L::KCH);
-        __syncwarp();
-        if (lane < L::KCH)
-          tma_load_4d(base + rg * L::QTILE + lane * L::QCHUNK, sg.own ? &maps.q_own : &maps.q_pre, lane * 64,
-                      sg.own ? sg.rc * ITEM + w * 128 : 0, sg.hk, sg.own ? sg.b : sg.b + w * p.seqs,
-                      bar(L::BAR_Q_FULL + rg));
-        ++q_count[rg];
-      }
-      if (NWG == 2 && !sg.pair) region ^= 1;
-      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++kv) {
-        const TileInfo x = tile_info<KT>(p, sg, t);
-        const int cur = page;
-        if (t + 1 < sg.t1) page = look_up(sg, t + 1);
-        const int boxes = (x.n + p.box_rows - 1) / p.box_rows;
-        for (int v = 0; v < 2; ++v) {
-          const long long i = 2 * kv + v;
-          const int st = (int)(i % NS);
-          if (!(ok = mbar_wait(bar(L::BAR_KV_EMPTY + st), ((uint32_t)(i / NS) & 1u) ^ 1u, wctx))) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar(L::BAR_KV_FULL + st), boxes * box_bytes * L::KCH);
-          __syncwarp();
-          if (has_box && row0 < x.n)
-            tma_load_4d(base + L::OFF_KV + st * L::SLOT + chunk * L::CHUNK + row0 * 128, v ? &maps.v : &maps.k,
-                        chunk * 64, (x.k0 + row0) & page_mask, sg.hk, cur, bar(L::BAR_KV_FULL + st));
-          ++issued;
-        }
-        if (!ok) break;
-      }
-    }
-    // every copy asked for has landed before the CTA may end (at once, unless a wait gave up)
-    for (long long i = issued > NS ? issued - NS : 0; i < issued; ++i)
-      drain_wait(bar(L::BAR_KV_FULL + (int)(i % NS)), (uint32_t)(i / NS) & 1u);
-    for (int rg = 0; rg < 2; ++rg)
-      if (q_count[rg] > 0) drain_wait(bar(L::BAR_Q_FULL + rg), (q_count[rg] - 1) & 1);
-  } else if (warp == 1) {
-    // ===================================================== products
-    if constexpr (NWG == 2) regs_dec<kRegsLow>();
-    const uint32_t leader = elect_one();
-    constexpr uint32_t idesc_qk = make_idesc(128, KT, BF, false, false);
-    constexpr uint32_t idesc_pv = make_idesc(128, D, BF, false, true);
-    const uint64_t dQ0 = make_sdesc_sw128(base, 16, 1024);
-    const uint64_t dK0 = make_sdesc_sw128(base + L::OFF_KV, 16, 1024);
-    const uint64_t dV0 = make_sdesc_sw128(base + L::OFF_KV, L::CHUNK, 1024);
-    bool ok = true;
-    // S side: its own walk, two steps ahead of the P V side
-    Seg a;
-    a.steps = 0;
-    int a_step = 0, a_region = 0, q_use[2] = {0, 0};
-    long long a_kv = 0, a_total = 0;  // key tiles of earlier segments; steps so far
-    bool a_more = true;
-    auto issue_s = [&]() -> bool {
-      if (!a_more) return true;
-      if (a_step == a.steps) {
-        a_kv += a.steps > 0 ? a.t1 - a.t0 : 0;
-        if (a.steps > 0 && NWG == 2 && !a.pair) a_region ^= 1;
-        a_step = 0;
-        if (!(a_more = walk.next(a))) return true;
-      }
-      const int s = a_step++;
-      const int q = a.pair ? (s & 1) : 0;                 // query tile
-      const int rg = a.pair ? q : a_region;
-      const bool q_first = a.pair ? s < 2 : s == 0, q_last = a.pair ? s >= a.steps - 2 : s == a.steps - 1;
-      const long long i = 2 * (a_kv + (a.pair ? s >> 1 : s));
-      const int st = (int)(i % NS), sb = (int)(a_total & 1);
-      if (q_first) {
-        if (!mbar_wait(bar(L::BAR_Q_FULL + rg), q_use[rg] & 1, wctx)) return false;
-        ++q_use[rg];
-      }
-      if (!mbar_wait(bar(L::BAR_KV_FULL + st), (uint32_t)(i / NS) & 1u, wctx)) return false;
-      tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        mma_ss(tmem + L::T_S(sb), sdesc_add(dQ0, rg * L::QTILE + (k / 4) * L::QCHUNK + (k % 4) * 32),
-               sdesc_add(dK0, st * L::SLOT + (k / 4) * L::CHUNK + (k % 4) * 32), idesc_qk, k > 0 ? 1u : 0u, leader);
-      }
-      mma_commit(bar(L::BAR_S_FULL + sb), leader);
-      if (!a.pair || q == 1) mma_commit(bar(L::BAR_KV_EMPTY + st), leader);
-      if (q_last) mma_commit(bar(L::BAR_Q_EMPTY + rg), leader);
-      ++a_total;
-      return true;
-    };
-    ok = issue_s() && issue_s();
-    Walk<D> pv_walk(p, start);
-    long long kv = 0, total = 0;
-    int o_use[2] = {0, 0}, p_cnt[2] = {0, 0};
-    while (ok && pv_walk.next(sg)) {
-      bool o_begun[2] = {false, false};
-      for (int s = 0; s < sg.steps && ok; ++s, ++total) {
-        const int sb = (int)(total & 1), w = NWG == 2 ? sb : 0;
-        const long long i = 2 * (kv + (sg.pair ? s >> 1 : s)) + 1;
-        const int st = (int)(i % NS);
-        if (!o_begun[w]) {  // the accumulator's last results have been read
-          if (o_use[w] > 0 && !(ok = mbar_wait(bar(L::BAR_O_FREE + w), (o_use[w] - 1) & 1, wctx))) break;
-          ++o_use[w];
-        }
-        if (!(ok = mbar_wait(bar(L::BAR_KV_FULL + st), (uint32_t)(i / NS) & 1u, wctx))) break;
-        if (!(ok = mbar_wait(bar(L::BAR_P_FULL + sb), p_cnt[sb] & 1, wctx))) break;
-        ++p_cnt[sb];
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < KT / 16; ++k) {
-          mma_ts(tmem + L::T_O(w), tmem + L::T_S(sb) + k * 8, sdesc_add(dV0, st * L::SLOT + k * 2048), idesc_pv,
-                 (o_begun[w] || k > 0) ? 1u : 0u, leader);
-        }
-        o_begun[w] = true;
-        if (!sg.pair || (s & 1)) mma_commit(bar(L::BAR_KV_EMPTY + st), leader);
-        if (NWG == 1) mma_commit(bar(L::BAR_PV_DONE), leader);
-        if (s == sg.steps - 1 || (sg.pair && s == sg.steps - 2)) mma_commit(bar(L::BAR_O_FULL + w), leader);
-        ok = issue_s();
-      }
-      kv += sg.t1 - sg.t0;
-    }
-    mma_commit(bar(L::BAR_MMA_DONE), leader);
-    drain_wait(bar(L::BAR_MMA_DONE), 0);
-  } else if (warp < 4) {
-    if constexpr (NWG == 2) regs_dec<kRegsLow>();
-  } else {
-    // ===================================================== softmax
-    if constexpr (NWG == 2) regs_inc<kRegsHigh>();
-    const int w = (warp - 4) >> 2;
-    const int wq = warp & 3;
-    const int row = wq * 32 + lane;
-    const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-    float2* stat = reinterpret_cast<float2*>(gbase + L::OFF_STAT);
-    bool ok = true;
-    long long kv = 0, total = 0;  // key tiles and steps of earlier segments
-    int s_cnt[2] = {0, 0};        // steps in each S buffer
-    int o_cnt = 0;                // segments that this warpgroup ended
-    int stat_cnt = 0;             // statistics handed over (by either warpgroup)
-    while (ok && walk.next(sg)) {
-      const int p0 = (int)(total & 1);
-      const int s_first = NWG == 2 ? (w ^ p0) : 0;
-      const int s_by = NWG == 2 ? 2 : 1;
-      const int tile_q = sg.pair ? s_first : 0;  // this warpgroup's query tile
-      // rows of the tile, and this row's sequence or token
-      int live;
-      if (sg.own)
-        live = min(128, p.R - sg.rc * ITEM - tile_q * 128);
-      else
-        live = min(p.seqs, p.B - sg.b - tile_q * p.seqs) * p.R;
-      const bool warp_live = wq * 32 < live;
-      bool counts = row < live;  // rows of a sequence that is not there may hold anything
-      if (counts && !sg.own) counts = p.lens[sg.b + tile_q * p.seqs + row / p.R] >= 0;
-      int own_lim = sg.visible;
-      if (sg.own && p.causal) own_lim = sg.len - p.T + (sg.rc * ITEM + tile_q * 128 + row) % p.T + 1;
-      float m = -INFINITY, l = 0.f;
-      bool mine = false;
-      for (int s = s_first; s < sg.steps; s += s_by) {
-        const int sb = NWG == 2 ? w : (int)((total + s) & 1);
-        const int kt = sg.pair ? s >> 1 : s;
-        const TileInfo x = tile_info<KT>(p, sg, sg.t0 + kt);
-        if (x.n < KT && (!sg.pair || s_first == 0)) {
-          // the tile ends behind the last token: rows x.n .. of V are whatever was there before
-          const long long i = 2 * (kv + kt) + 1;
-          const int st = (int)(i % NS);
-          if (!(ok = mbar_wait(bar(L::BAR_KV_FULL + st), (uint32_t)(i / NS) & 1u, wctx))) break;
-          const int n16 = (KT - x.n) * 8;  // 16-byte units per chunk: whole rows, so the swizzle does not matter
-          for (int c = 0; c < L::KCH; ++c)
-            for (int z = (int)threadIdx.x & 127; z < n16; z += 128)
-              *reinterpret_cast<uint4*>(gbase + L::OFF_KV + st * L::SLOT + c * L::CHUNK + x.n * 128 + z * 16) =
-                  make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
-        if (!(ok = mbar_wait(bar(L::BAR_S_FULL + sb), s_cnt[sb] & 1, wctx))) break;
-        ++s_cnt[sb];
-        tc_fence_after();
-        if (warp_live) {
-          const int lim = x.pre ? x.n : min(x.n, own_lim - x.k0);
-          ok = softmax_step<D, BF>(tmem + lanes + L::T_S(sb), tmem + lanes + L::T_O(w), p.scale_log2, lim, !mine, m, l,
-                                   [&]() -> bool {
-                                     // one accumulator: the previous step's product may still run
-                                     if constexpr (NWG == 1)
-                                       return mbar_wait(bar(L::BAR_PV_DONE), (uint32_t)(total + s - 1) & 1u, wctx);
-                                     return true;
-                                   });
-          if (!ok) break;
-          // weights are at most 2^8: a sum that is no finite number came from a non-finite score
-          // (a wrong page may be the reason, and that report stays)
-          if (counts && !(l <= 3.0e38f)) atomicCAS(p.err, kDevOk, kDevRange);
-          tmem_wait_st();
-        }
-        mine = true;
-        tc_fence_before();
-        mbar_arrive(bar(L::BAR_P_FULL + sb));
-      }
-      total += sg.steps;
-      kv += sg.t1 - sg.t0;
-      if (!ok) break;
-      if (!mine) continue;
-      // ---- the end of a segment.  Two tiles: each warpgroup has its own rows.  One tile: the
-      // warpgroup of the last step joins the other's m, l (through shared memory) and O.
-      const bool other = NWG == 2 && !sg.pair && sg.steps > 1;
-      const bool ends = sg.pair || NWG == 1 || ((int)(total - 1) & 1) == w;
-      if (other) {
-        if (!ends) {
-          if (stat_cnt > 0 && !(ok = mbar_wait(bar(L::BAR_STAT_EMPTY), (stat_cnt - 1) & 1, wctx))) break;
-          stat[row] = make_float2(m, l);
-          mbar_arrive(bar(L::BAR_STAT_FULL));
-          ++stat_cnt;
-          continue;
-        }
-        if (!(ok = mbar_wait(bar(L::BAR_STAT_FULL), stat_cnt & 1, wctx))) break;
-        ++stat_cnt;
-      }
-      float2 theirs = make_float2(-INFINITY, 0.f);
-      if (other) {
-        theirs = stat[row];
-        mbar_arrive(bar(L::BAR_STAT_EMPTY));
-      }
-      if (!(ok = mbar_wait(bar(L::BAR_O_FULL + w), o_cnt & 1, wctx))) break;
-      ++o_cnt;
-      tc_fence_after();
-      const float M = fmaxf(m, theirs.x);
-      float ca = M == -INFINITY ? 0.f : ex2_approx(m - M);
-      float cb = M == -INFINITY ? 0.f : ex2_approx(theirs.x - M);
-      const float sum = ca * l + cb * theirs.y;
-      const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
-      const bool direct = whole && sg.own && (!p.packed || p.prefix_len == 0);
-      const long long item = sg.own ? ((long long)sg.b * p.n_rc + sg.rc) * p.H_kv + sg.hk
-                                    : (long long)sg.hk * p.n_groups + sg.b / (p.seqs * NWG);
-      const long long items = sg.own ? (p.packed ? (long long)p.B * p.n_rc * p.H_kv : 0) : (long long)p.n_groups * p.H_kv;
-      const int part = sg.own ? p.ctas - 1 - (int)blockIdx.x : (int)blockIdx.x;
-      const long long slot = whole ? item : items + 2 * part + (sg.t0 == 0 ? 1 : 0);
-      const int slot_rows = sg.own ? min(p.R, ITEM) : ITEM;
-      const int in_slot = tile_q * 128 + wq * 32;  // first row of this warp in the slot
-      const long long out_row = ((long long)sg.b * p.H_kv + sg.hk) * p.R + sg.rc * ITEM + in_slot;
-      if (sg.own && sg.t0 == 0 && tile_q == 0 && row == 0) {
-        // for the joining kernel: which parts of the line hold the item
-        int last = part;
-        if (!whole) {  // the item's last unit is nt - t1 units behind this part
-          const int parts = line_parts(p, start.total);
-          last = part_of(start.total, parts, part_begin(start.total, parts, part + 1) + (sg.nt - sg.t1) - 1);
-        }
-        p.seg[item] = make_int2(part, last);
-      }
-      const int left = live - wq * 32;  // live rows of this warp
-      if (direct) {
-        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-        ca *= inv;
-        cb *= inv;
-      }
-      const uint32_t tO = tmem + lanes + L::T_O(w), tO2 = tmem + lanes + L::T_O(w ^ 1);
-      auto load = [&](int c, uint32_t (&u)[32]) {  // 32 columns of the joined O
-        tmem_ld32(tO + 32 * c, u);
-        if (other) {
-          uint32_t v[32];
-          tmem_ld32(tO2 + 32 * c, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            u[i] = __float_as_uint(fmaf(ca, __uint_as_float(u[i]), cb * __uint_as_float(v[i])));
-        } else {
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(ca * __uint_as_float(u[i]));
-        }
-        if (c == D / 32 - 1) {  // everything read
-          tc_fence_before();
-          mbar_arrive(bar(L::BAR_O_FREE + w));
-          if (other) mbar_arrive(bar(L::BAR_O_FREE + (w ^ 1)));
-        }
-      };
-      if (direct) {
-        uint8_t* dst = static_cast<uint8_t*>(p.o) + out_row * (2 * D);
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint4 a[8];
-          uint32_t u[32];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            load(2 * c + h, u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              auto at = [&](int k) { return __uint_as_float(u[8 * i + k]); };
-              // a row that saw nothing has P = 0 and an accumulator of zeros
-              a[4 * h + i] = make_uint4(pack16<BF>(at(0), at(1)), pack16<BF>(at(2), at(3)), pack16<BF>(at(4), at(5)),
-                                        pack16<BF>(at(6), at(7)));
-            }
-          }
-          warp_store_rows_128b(a, dst + c * 128, 2 * D, 0, left);
-        }
-        if (p.lse != nullptr && lane < left)
-          p.lse[out_row + lane] = sum > 0.f ? (M + __log2f(sum)) * 0.69314718055994531f : -INFINITY;
-      } else {
-        const long long srow = slot * slot_rows + in_slot;
-        float* part = (sg.own ? p.own_o : p.pre_o) + srow * D;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t u[32];
-          load(c, u);
-          uint4 a[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-          warp_store_rows_128b(a, reinterpret_cast<uint8_t*>(part) + c * 128, 4 * D, 0, left);
-        }
-        if (lane < left) (sg.own ? p.own_ml : p.pre_ml)[srow + lane] = make_float2(M, sum);
-      }
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
+  // Both lines in one phase where they take the same form, else one phase each.
+  const bool pre = p.packed && p.prefix_len > 0, both = !pre || p.pre_few == p.own_few;
+  const bool own_first = (blockIdx.x & 1) != 0;
+  const int phases = both ? 1 : 2;
+  auto phase_end = [] {
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();  // the phases share the ring and tensor memory
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+  };
+  if (warp < 4) {
+    regs_dec<kRegsLow>();
+#pragma unroll 1
+    for (int phase = 0; phase < phases; ++phase) {
+      const bool do_own = both || (phase == 0) == own_first, do_pre = pre && (both || !do_own);
+      if (do_own ? p.own_few : p.pre_few)
+        few_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::FEW_BAR, tmem, wctx);
+      else
+        dense_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::DENSE_BAR, tmem, wctx);
+      phase_end();
+    }
+  } else {
+    regs_inc<kRegsHigh>();
+#pragma unroll 1
+    for (int phase = 0; phase < phases; ++phase) {
+      const bool do_own = both || (phase == 0) == own_first, do_pre = pre && (both || !do_own);
+      if (do_own ? p.own_few : p.pre_few)
+        few_softmax<D, BF>(p, start, do_pre, do_own, gbase, bars + 8u * M::FEW_BAR, tmem, wctx);
+      else
+        dense_softmax<D, BF>(p, start, do_pre, do_own, gbase, bars + 8u * M::DENSE_BAR, tmem, wctx);
+      phase_end();
+    }
   }
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------- joining the parts
 // One warp per query row.  Parts of the own keys, then of the prefix, in the order of their lines.
 template <int D, bool BF>
 __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p) {
-  constexpr int NWG = PLayout<D>::NWG, KT = PLayout<D>::KT, ITEM = 128 * NWG;
+  constexpr int NWG = Dense<D>::NWG, ITEM = 128 * NWG;
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // (b * H + h) * T + t
@@ -799,7 +1294,7 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   const int len = own_len(p, b);
   if (len < 0) return;
   const int rc = r / ITEM;
-  const int nt = own_tiles<KT>(p, len, own_visible<ITEM>(p, len, rc));
+  const int nt = own_tiles(p, len, own_visible<ITEM>(p, len, rc));
   const bool pre = p.packed && p.prefix_len > 0;
   const long long item = ((long long)b * p.n_rc + rc) * p.H_kv + hk;
   int2 own = make_int2(0, -1), pc = make_int2(0, -1);
@@ -870,16 +1365,16 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
 #pragma unroll
   for (int i = 0; i < E; i += 2) dst[i / 2] = pack16<BF>(o[i] * inv, o[i + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
-    p.lse[row] = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
+    p.lse[row] = log_sum(M, L);
 }
 
 template <int D, bool BF>
 cudaError_t launch(const PagedMaps& maps, const PagedParams& p, cudaStream_t s) {
-  using L = PLayout<D>;
+  constexpr int smem = Smem<D>::ALLOC;
   auto kernel = fa_paged_attn_sm100_kernel<D, BF>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM_ALLOC);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<p.ctas, L::THREADS, L::SMEM_ALLOC, s>>>(maps, p);
+  kernel<<<p.ctas, kThreads, smem, s>>>(maps, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = (long long)p.B * p.H * p.T;
   fa_paged_join_kernel<D, BF><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
