@@ -822,11 +822,11 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 }
 
 // A warpgroup's work on one segment with up to N rows (N = 8, 16 or 32): thread k has key k of
-// every tile and, in the end, column k of O.
+// every tile and, in the end, column k of O.  False (for all threads) if a bounded wait gave up.
 template <int D, bool BF, int N>
 __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& start, const Seg& sg, uint32_t bars,
                                             uint8_t* gbase, uint32_t tmem, const WaitCtx& wctx, int w, uint32_t kv,
-                                            uint32_t seg_no) {
+                                            uint32_t seg_no, uint32_t& s_no) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS;
   constexpr int ITEM = 128 * Dense<D>::NWG;
@@ -843,11 +843,14 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
     m[r] = -INFINITY;
     l[r] = 0.f;
   }
+  // A wait that gave up leaves ok false, and the segment goes on to its end all the same: the
+  // barriers among the warpgroup need all of its threads.
+  bool ok = true;
   const int n_tiles = sg.t1 - sg.t0;
-  for (int t = 0; t < n_tiles; ++t) {
+  for (int t = 0; t < n_tiles; ++t, ++s_no) {
     const uint32_t n = kv + t;  // step of the phase
     const TileInfo x = tile_info(p, sg, sg.t0 + t);
-    if (!mbar_wait(bar(L::S_FULL + (n & 3u)), n / 4 & 1u, wctx)) return false;
+    ok &= mbar_wait(bar(L::S_FULL + 2 * w + (s_no & 1u)), s_no / 2 & 1u, wctx);
     tc_fence_after();
     float s[N];
     {
@@ -897,7 +900,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
       }
       if (moved && t > 0) {  // (the same for all threads)
         // O^T holds the earlier tiles once their products have completed
-        if (!mbar_wait(bar(L::P_EMPTY + ((n - 1) & 1u)), (n - 1) / 2 & 1u, wctx)) return false;
+        ok &= mbar_wait(bar(L::P_EMPTY + ((n - 1) & 1u)), (n - 1) / 2 & 1u, wctx);
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < L::PARTS; ++h) {
@@ -912,7 +915,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
       }
     }
     // P^T: row r of the buffer holds the weights of query row r, 64 keys to a 128-byte row of a chunk
-    if (n >= 2 && !mbar_wait(bar(L::P_EMPTY + (n & 1u)), (n / 2 - 1) & 1u, wctx)) return false;
+    if (n >= 2) ok &= mbar_wait(bar(L::P_EMPTY + (n & 1u)), (n / 2 - 1) & 1u, wctx);
     uint8_t* pb = gbase + L::OFF_P + (n & 1u) * 2 * L::RCHUNK + (key >> 6) * L::RCHUNK + (key & 7) * 2;
     const uint32_t unit = (uint32_t)(key & 63) >> 3;
 #pragma unroll
@@ -926,7 +929,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
 #pragma unroll
       for (int h = 0; h < L::PARTS; ++h) {
         const uint32_t i = (2 * n + 1) * L::PARTS + h, st = i % NS;
-        if (!mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx)) return false;
+        ok &= mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx);
         zero_rows(gbase + st * L::SLOT, L::PCH, L::CHUNK, x.n);
       }
     }
@@ -961,7 +964,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
       else if (p.lse != nullptr)
         p.lse[out_row + r] = log_sum(m[r], total[r]);
     }
-  if (!mbar_wait(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx)) return false;
+  ok &= mbar_wait(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
   tc_fence_after();
   uint32_t u[L::PARTS][N];
 #pragma unroll
@@ -984,7 +987,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
           (sg.own ? p.own_o : p.pre_o)[(pl.slot_row + r) * D + col] = v;
       }
   }
-  return true;
+  return !group_any(id, !ok);
 }
 
 // Warps 0 - 3: copies and products.
@@ -1067,6 +1070,7 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
     };
     int t = 0, n_tiles = 0;
     uint32_t n_s = 0, seg_no = 0xffffffffu, cols = 0;
+    uint32_t s_no0 = 0, s_no1 = 0;  // steps of each warpgroup: it waits for its own only, so they have their own barriers
     bool more = true;
     auto issue_s = [&]() -> Step {
       Step f{};
@@ -1094,7 +1098,8 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
                  (h > 0 || k > 0) ? 1u : 0u, leader);
         mma_commit(bar(L::KV_EMPTY + st), leader);
       }
-      mma_commit(bar(L::S_FULL + (n_s & 3u)), leader);
+      const uint32_t w = seg_no & 1u;
+      mma_commit(bar(L::S_FULL + 2 * w + ((w ? s_no1++ : s_no0++) & 1u)), leader);
       if (t == n_tiles - 1) mma_commit(bar(L::Q_EMPTY + qb), leader);
       f.valid = true;
       f.first = t == 0;
@@ -1142,13 +1147,13 @@ __device__ __forceinline__ void few_softmax(const PagedParams& p, const Start& s
   Walk<128 * Dense<D>::NWG> walk(p, start, pre, own);
   Seg sg;
   const int w = (int)(threadIdx.x >> 7) - 1;
-  uint32_t kv = 0, seg_no = 0;
+  uint32_t kv = 0, seg_no = 0, s_no = 0;
   for (; walk.next(sg); kv += sg.t1 - sg.t0, ++seg_no) {
     if ((seg_no & 1u) != (uint32_t)w) continue;
     const int rows = sg.own ? p.R : p.R * p.B;
-    const bool ok = rows <= 8    ? few_segment<D, BF, 8>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no)
-                    : rows <= 16 ? few_segment<D, BF, 16>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no)
-                                 : few_segment<D, BF, 32>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no);
+    const bool ok = rows <= 8    ? few_segment<D, BF, 8>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                    : rows <= 16 ? few_segment<D, BF, 16>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                                 : few_segment<D, BF, 32>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no);
     if (!ok) break;
   }
 }

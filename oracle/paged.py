@@ -19,8 +19,9 @@ def gather(pages: np.ndarray, table, n: int) -> np.ndarray:
     """The first n tokens that `table` names, (H_kv, n, d)."""
     _, h, ps, d = pages.shape
     out = np.zeros((h, n, d))
-    for j in range(n):
-        out[:, j] = pages[table[j // ps], :, j % ps]
+    for j in range(0, n, ps):
+        m = min(ps, n - j)
+        out[:, j:j + m] = pages[table[j // ps], :, :m]
     return out
 
 
@@ -40,23 +41,23 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, prefix_table, pr
             continue
         ks = np.concatenate([pre_k, gather(kp, table[b], lens[b])], axis=1)
         vs = np.concatenate([pre_v, gather(vp, table[b], lens[b])], axis=1)
-        for h in range(H):
-            for t in range(T):
-                own = max(0, lens[b] - T + t + 1) if causal else lens[b]
-                n = prefix_len + own
-                count[b, h, t] = n
-                if n == 0:
-                    o[b, h, t], lse[b, h, t] = 0.0, -np.inf
-                    continue
-                k, v = ks[h // group, :n], vs[h // group, :n]
-                s = scale * (k @ q[b, h, t])
-                m = s.max()
-                e = np.exp(s - m)
-                o[b, h, t] = (e @ v) / e.sum()
-                lse[b, h, t] = m + np.log(e.sum())
-                mean_abs[b, h, t] = (e @ np.abs(v)) / e.sum()
-                sum_abs[b, h, t] = np.abs(v).sum(0)
-                big[b, h, t] = scale * (np.abs(k) @ np.abs(q[b, h, t])).max()
+        own = np.array([max(0, lens[b] - T + t + 1) if causal else lens[b] for t in range(T)])
+        n = prefix_len + own  # keys that each query sees: the first n
+        count[b] = n
+        seen = np.arange(ks.shape[1]) < n[:, None]
+        some = n > 0
+        o[b][:, ~some], lse[b][:, ~some] = 0.0, -np.inf
+        for h in range(H if some.any() else 0):
+            k, v = ks[h // group], vs[h // group]
+            s = np.where(seen, scale * (q[b, h] @ k.T), -np.inf)[some]
+            m = s.max(axis=1, keepdims=True)
+            e = np.exp(s - m)
+            total = e.sum(axis=1, keepdims=True)
+            o[b, h, some] = (e @ v) / total
+            lse[b, h, some] = (m + np.log(total))[:, 0]
+            mean_abs[b, h, some] = (e @ np.abs(v)) / total
+            sum_abs[b, h, some] = seen[some] @ np.abs(v)
+            big[b, h, some] = (scale * (np.abs(q[b, h]) @ np.abs(k).T) * seen).max(axis=1)[some]
     return o, lse, mean_abs, sum_abs, big, count
 
 

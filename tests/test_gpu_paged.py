@@ -158,6 +158,16 @@ def test_a_long_sequence_beside_short_ones():
     case([9000, 1, 30, 4000], 0, 4, 1, 1, 64, 64)
 
 
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 32), (256, 64)])
+@pytest.mark.parametrize("group,T", [(1, 1), (4, 1), (4, 3), (4, 5), (4, 10), (4, 40)])
+def test_many_tiles_for_every_multiprocessor(d, ps, group, T):
+    # some 900 (item, key tile) pairs: every multiprocessor walks over several items, some of many tiles
+    rng = np.random.default_rng(d + T)
+    lens = [int(x) for x in rng.integers(0, 1500, 12)] + [1, 3000]
+    case(lens, 1100, 8 * group, 8, T, d, ps)
+    case(lens, 0, 8 * group, 8, T, d, ps, F16)
+
+
 def test_a_large_scale_and_equal_scores():
     c = Cache([200, 3], 100, 2, 64, 16, BF16, seed=4)
     q = c.queries(4, 1)
