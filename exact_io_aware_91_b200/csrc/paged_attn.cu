@@ -113,7 +113,8 @@ struct Smem {
   static constexpr int OFF_SCAN = OFF_START + 48;  // long long[12]
   static constexpr int OFF_TMEM_SLOT = OFF_SCAN + 96;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
-  static constexpr int ALLOC = OFF_ABORT + 8 + 1024;
+  static constexpr int OFF_ISSUED = OFF_ABORT + 8;  // uint32[2]: ring index behind the last K and V slot asked for
+  static constexpr int ALLOC = OFF_ISSUED + 8 + 1024;
   static_assert(ALLOC <= 232448, "shared memory per CTA");
 };
 
@@ -121,6 +122,23 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+  }
+}
+
+// After a phase in which a wait gave up: every K and V copy asked for has landed (or the bounded
+// waits run out).  `asked[v]` is the ring index behind the last slot that the K (v = 0) or V warp asked
+// for, `parts` slots make a tile; the last index of a slot tells its barrier's phase.
+template <int NS>
+__device__ __forceinline__ void drain_ring(uint32_t bar_full, int parts, const volatile uint32_t* asked) {
+  for (uint32_t s = 0; s < NS; ++s) {
+    int last = -1;
+    for (int v = 0; v < 2; ++v)
+      for (int k = (int)asked[v] - 1; k >= 0 && k >= (int)asked[v] - 4 * NS; --k)
+        if ((uint32_t)k % NS == s && (k / parts & 1) == v) {
+          last = max(last, k);
+          break;
+        }
+    if (last >= 0) drain_wait(bar_full + 8u * s, (uint32_t)last / NS & 1u);
   }
 }
 
@@ -496,7 +514,7 @@ __device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, 
 template <int D, bool BF>
 __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedParams& p, const Start& start, bool pre,
                                             bool own, uint32_t base, uint32_t bars, uint32_t tmem,
-                                           const WaitCtx& wctx) {
+                                           volatile uint32_t* asked_for, const WaitCtx& wctx) {
   using L = Dense<D>;
   constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
   constexpr uint32_t NS = L::NS;
@@ -554,9 +572,8 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
         issued = i + 1;
       }
     }
-    // every copy asked for has landed before the phase ends (at once, unless a wait gave up)
-    for (uint32_t k = issued > NS ? issued - NS : 0; k < issued; ++k)
-      if ((k & 1u) == (uint32_t)v) drain_wait(bar(L::KV_FULL + k % NS), k / NS & 1u);
+    if (lane == 0) asked_for[v] = issued;
+    // the copies of Q have landed before the phase ends (at once, unless a wait gave up)
     for (int rg = 0; rg < 2; ++rg)
       if (q_count[rg] > 0) drain_wait(bar(L::Q_FULL + rg), (q_count[rg] - 1) & 1);
   } else if (warp == 1) {
@@ -994,7 +1011,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
 template <int D, bool BF>
 __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParams& p, const Start& start, bool pre,
                                           bool own, uint32_t base, uint32_t bars, uint32_t tmem,
-                                         const WaitCtx& wctx) {
+                                         volatile uint32_t* asked_for, const WaitCtx& wctx) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS, NQ = L::NQ;
   constexpr int PARTS = L::PARTS, ITEM = 128 * Dense<D>::NWG;
@@ -1048,9 +1065,8 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
         }
       }
     }
-    // every copy asked for has landed before the phase ends (at once, unless a wait gave up)
-    for (uint32_t k = issued > NS ? issued - NS : 0; k < issued; ++k)
-      if ((k / PARTS & 1u) == (uint32_t)v) drain_wait(bar(L::KV_FULL + k % NS), k / NS & 1u);
+    if (lane == 0) asked_for[v] = issued;
+    // the copies of Q have landed before the phase ends (at once, unless a wait gave up)
     if (v == 0)
       for (uint32_t k = seg_no > NQ ? seg_no - NQ : 0; k < seg_no; ++k)
         drain_wait(bar(L::Q_FULL + k % NQ), k / NQ & 1u);
@@ -1253,11 +1269,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool pre = p.packed && p.prefix_len > 0, both = !pre || p.pre_few == p.own_few;
   const bool own_first = (blockIdx.x & 1) != 0;
   const int phases = both ? 1 : 2;
-  auto phase_end = [] {
+  volatile uint32_t* asked_for = reinterpret_cast<volatile uint32_t*>(gbase + M::OFF_ISSUED);
+  // False if a wait gave up: the CTA ends then.
+  auto phase_end = [&](bool few) -> bool {
     __syncwarp();
     tc_fence_before();
     __syncthreads();  // the phases share the ring and tensor memory
     tc_fence_after();
+    if (!*abort_flag) return true;
+    if (threadIdx.x == 0) {
+      if (few)
+        drain_ring<Few<D>::NS>(bars + 8u * (M::FEW_BAR + Few<D>::KV_FULL), Few<D>::PARTS, asked_for);
+      else
+        drain_ring<Dense<D>::NS>(bars + 8u * (M::DENSE_BAR + Dense<D>::KV_FULL), 1, asked_for);
+    }
+    __syncthreads();
+    return false;
   };
   if (warp < 4) {
     regs_dec<kRegsLow>();
@@ -1265,10 +1292,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int phase = 0; phase < phases; ++phase) {
       const bool do_own = both || (phase == 0) == own_first, do_pre = pre && (both || !do_own);
       if (do_own ? p.own_few : p.pre_few)
-        few_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::FEW_BAR, tmem, wctx);
+        few_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::FEW_BAR, tmem, asked_for, wctx);
       else
-        dense_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::DENSE_BAR, tmem, wctx);
-      phase_end();
+        dense_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::DENSE_BAR, tmem, asked_for, wctx);
+      if (!phase_end(do_own ? p.own_few : p.pre_few)) break;
     }
   } else {
     regs_inc<kRegsHigh>();
@@ -1279,7 +1306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         few_softmax<D, BF>(p, start, do_pre, do_own, gbase, bars + 8u * M::FEW_BAR, tmem, wctx);
       else
         dense_softmax<D, BF>(p, start, do_pre, do_own, gbase, bars + 8u * M::DENSE_BAR, tmem, wctx);
-      phase_end();
+      if (!phase_end(do_own ? p.own_few : p.pre_few)) break;
     }
   }
   if (warp == 1) tmem_dealloc(tmem, 512);
