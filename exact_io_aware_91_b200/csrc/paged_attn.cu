@@ -35,7 +35,10 @@
 // In both, warp 0 looks up pages and streams Q and K tiles with TMA, warp 2 V tiles, into one ring (a
 // lane issues the box of a piece of a page; two warps, because a box costs its issuer some 70
 // cycles and 8-token pages make 32 of them per tile), and warp 1 issues the tensor-core products, S
-// of a step two steps ahead of its P V, across items.
+// of a step two steps ahead of its P V, across items.  Warp 3 walks the lines and hands the others what
+// they need to know of each segment through shared memory: code that every role runs once per
+// segment is code that none of them finds in the instruction cache (with a walk in each role,
+// segments of one tile took 8000 cycles).
 //
 // What lies behind a sequence's last token in a page never enters: its scores are masked, and the rows of
 // the V tile are set to zero in shared memory (0 x NaN would be NaN).  P is rounded to the 16-bit
@@ -50,7 +53,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 384;  // warp 0: Q, K; 1: products; 2: V; 4-7 and 8-11: softmax
+constexpr int kThreads = 384;  // warp 0: Q, K; 1: products; 2: V; 3: schedule; 4-7 and 8-11: softmax
 // registers: the first four warps give theirs to the two softmax warpgroups
 constexpr uint32_t kRegsLaunch = 168, kRegsLow = 88, kRegsHigh = 208;
 static_assert(kRegsLow + 2 * kRegsHigh <= 3 * kRegsLaunch, "register split exceeds the launch budget");
@@ -65,7 +68,7 @@ struct Dense {
   static constexpr int QTILE = KCH * QCHUNK;
   static constexpr int CHUNK = KT * 128;             // one chunk of a K or V tile
   static constexpr int SLOT = KCH * CHUNK;
-  static constexpr int NS = D == 64 ? 12 : 5;        // ring slots
+  static constexpr int NS = D == 64 ? 11 : 5;        // ring slots
   static constexpr int OFF_KV = NWG * QTILE;
   static constexpr int OFF_STAT = OFF_KV + NS * SLOT;  // float2[128]: a warpgroup's m and l for the other
   static constexpr int END = OFF_STAT + 1024;
@@ -105,11 +108,28 @@ struct Few {
 };
 
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
+// One item, or the part of it that falls into a CTA's part of a line.
+struct Seg {
+  int valid, own, pair;  // pair: dense form, two query tiles
+  int b, hk, row0;       // prefix: b is the first sequence of tile 0; own: row0 is the first row of the item
+  int rows[2];           // rows of the query tiles (few form: of the item)
+  int len, visible;      // own: the sequence's length, and its keys seen by some row
+  int lead;              // key tiles below `lead` are the prefix's
+  int t0, t1;            // key tiles
+  int direct;            // the item is whole and nothing is to be joined: results go to o and lse
+  uint8_t* o_dst;        // first row's result (16-bit) or partial result (fp32)
+  void* ml_dst;          // first row's lse (float, or null), or its (maximum, sum)
+};
+constexpr int kSegRing = 4;
+constexpr int kSegReaders = 11;  // warps that read each segment
+
 template <int D>
 struct Smem {
   static constexpr int OFF_BAR = cmax(Dense<D>::END, Few<D>::END);
-  static constexpr int DENSE_BAR = 0, FEW_BAR = Dense<D>::NBAR;
-  static constexpr int OFF_START = OFF_BAR + (Dense<D>::NBAR + Few<D>::NBAR) * 8;
+  static constexpr int DENSE_BAR = 0, FEW_BAR = Dense<D>::NBAR, SEG_FULL = FEW_BAR + Few<D>::NBAR;
+  static constexpr int SEG_EMPTY = SEG_FULL + kSegRing, NBAR = SEG_EMPTY + kSegRing;
+  static constexpr int OFF_SEG = OFF_BAR + NBAR * 8;
+  static constexpr int OFF_START = OFF_SEG + kSegRing * (int)sizeof(Seg);
   static constexpr int OFF_SCAN = OFF_START + 48;  // long long[12]
   static constexpr int OFF_TMEM_SLOT = OFF_SCAN + 96;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
@@ -271,26 +291,17 @@ struct Start {  // where a CTA's part of the own line begins
   int b, rc, hk, at;  // item, and the unit inside it
 };
 
-// One item, or the part of it that falls into a CTA's part of the line.
-struct Seg {
-  bool own;
-  int b, rc, hk;   // prefix: b is the first sequence of tile 0
-  int len;         // own: the sequence's length
-  int visible;     // own: keys seen by some row
-  int t0, t1, nt;  // key tiles t0 .. t1 - 1 of nt
-  bool pair;       // dense: two query tiles
-};
-
-// Walks a CTA's segments of one line or both; every role does so for itself.
-template <int ITEM>
+// Walks a CTA's segments of one line or both.
+template <int D>
 struct Walk {
+  static constexpr int NWG = Dense<D>::NWG, ITEM = 128 * NWG;
   const PagedParams& p;
+  const Start& start;
   long long pre_u, pre_end, own_left;
   int b, rc, hk, at;
   int cur_b, len;
-  bool own_first;
 
-  __device__ Walk(const PagedParams& p_, const Start& s, bool pre, bool own) : p(p_) {
+  __device__ Walk(const PagedParams& p_, const Start& s, bool pre, bool own) : p(p_), start(s) {
     const long long n = pre ? (long long)p.n_groups * p.H_kv * p.pre_tiles : 0;
     const int parts = line_parts(p, n), c = blockIdx.x;
     pre_u = c < parts ? part_begin(n, parts, c) : 0;
@@ -302,27 +313,38 @@ struct Walk {
     at = s.at;
     cur_b = -1;
     len = 0;
-    own_first = (blockIdx.x & 1) != 0;
   }
-  __device__ bool next(Seg& s) {
-    if (own_first && own_left > 0) {
-      if (next_own(s)) return true;
+  // Where the results go.
+  __device__ void place(Seg& s, bool whole, long long item, long long items, int part, int item_rows, long long out_row) {
+    s.direct = whole && s.own && (!p.packed || p.prefix_len == 0);
+    if (s.direct) {
+      s.o_dst = static_cast<uint8_t*>(p.o) + out_row * (2 * D);
+      s.ml_dst = p.lse != nullptr ? p.lse + out_row : nullptr;
+    } else {
+      const long long row = (whole ? item : items + 2 * part + (s.t0 == 0 ? 1 : 0)) * item_rows;
+      s.o_dst = reinterpret_cast<uint8_t*>((s.own ? p.own_o : p.pre_o) + row * D);
+      s.ml_dst = (s.own ? p.own_ml : p.pre_ml) + row;
     }
+  }
+  __device__ bool next(Seg& s, bool own_first) {
+    if (own_first && next_own(s)) return true;
     if (pre_u < pre_end) {
-      const int item = (int)(pre_u / p.pre_tiles);
-      s.own = false;
-      s.hk = item / p.n_groups;
-      s.b = (item - s.hk * p.n_groups) * p.seqs * (ITEM / 128);
-      s.rc = 0;
-      s.len = s.visible = 0;
-      s.nt = p.pre_tiles;
-      s.t0 = (int)(pre_u - (long long)item * p.pre_tiles);
-      s.t1 = (int)min((long long)s.nt, s.t0 + (pre_end - pre_u));
-      s.pair = ITEM == 256 && s.b + p.seqs < p.B;
+      const long long item = pre_u / p.pre_tiles;
+      s.own = 0;
+      s.hk = (int)(item / p.n_groups);
+      s.b = (int)(item - (long long)s.hk * p.n_groups) * p.seqs * NWG;
+      s.row0 = s.len = s.visible = 0;
+      s.lead = p.pre_tiles;
+      s.t0 = (int)(pre_u - item * p.pre_tiles);
+      s.t1 = (int)min((long long)p.pre_tiles, s.t0 + (pre_end - pre_u));
+      s.pair = NWG == 2 && s.b + p.seqs < p.B;
+      s.rows[0] = min(p.seqs, p.B - s.b) * p.R;
+      s.rows[1] = s.pair ? min(p.seqs, p.B - s.b - p.seqs) * p.R : 0;
       pre_u += s.t1 - s.t0;
+      place(s, s.t0 == 0 && s.t1 == p.pre_tiles, item, (long long)p.n_groups * p.H_kv, blockIdx.x, ITEM, 0);
       return true;
     }
-    return own_left > 0 && next_own(s);
+    return next_own(s);
   }
   __device__ bool next_own(Seg& s) {
     while (b < p.B && own_left > 0) {
@@ -340,7 +362,7 @@ struct Walk {
         own_left -= end - at;
       }
       at = 0;
-      s.rc = rc;
+      const int rc0 = rc;
       s.hk = hk;
       s.b = b;
       // past this item (a part that ends inside it has nothing left); an item without tiles has none
@@ -353,13 +375,28 @@ struct Walk {
         }
       }
       if (t1 > t0) {
-        s.own = true;
+        s.own = 1;
+        s.row0 = rc0 * ITEM;
+        s.rows[0] = min(128, p.R - s.row0);
+        s.rows[1] = NWG == 2 ? max(0, min(128, p.R - s.row0 - 128)) : 0;
+        s.pair = s.rows[1] > 0;
         s.len = len;
         s.visible = vis;
-        s.nt = nt;
+        s.lead = p.packed ? 0 : p.pre_tiles;
         s.t0 = t0;
         s.t1 = t1;
-        s.pair = ITEM == 256 && p.R - s.rc * 256 > 128;
+        const int part = p.ctas - 1 - (int)blockIdx.x;
+        const long long item = ((long long)s.b * p.n_rc + rc0) * p.H_kv + s.hk;
+        place(s, t0 == 0 && t1 == nt, item, p.packed ? (long long)p.B * p.n_rc * p.H_kv : 0, part, min(p.R, ITEM),
+              ((long long)s.b * p.H_kv + s.hk) * p.R + s.row0);
+        if (t0 == 0 && threadIdx.x % 32 == 0) {  // for the joining kernel: which parts of the line hold the item
+          int last = part;
+          if (t1 < nt) {  // its last unit is nt - t1 units behind this part
+            const int parts = line_parts(p, start.total);
+            last = part_of(start.total, parts, part_begin(start.total, parts, part + 1) + (nt - t1) - 1);
+          }
+          p.seg[item] = make_int2(part, last);
+        }
         return true;
       }
     }
@@ -368,48 +405,52 @@ struct Walk {
   }
 };
 
+// The segments' ring, as the readers see it: segment `no` of this CTA, copied out of shared memory.
+struct SegRing {
+  const Seg* ring;
+  uint32_t full, empty;  // barriers
+  uint32_t no;
+  __device__ __forceinline__ bool next(Seg& s, const WaitCtx& wctx) {
+    const uint32_t slot = no % kSegRing;
+    if (!mbar_wait(full + 8u * slot, no / kSegRing & 1u, wctx)) return false;
+    s = ring[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8u * slot);
+    ++no;
+    return s.valid != 0;
+  }
+};
+// Warp 3: the segments of a phase, and one that says that there are no more.
+template <int D>
+__device__ __forceinline__ void schedule(const PagedParams& p, const Start& start, bool pre, bool own, bool own_first,
+                                         Seg* ring, uint32_t full, uint32_t empty, uint32_t& no, const WaitCtx& wctx) {
+  Walk<D> walk(p, start, pre, own);
+  for (bool more = true; more; ++no) {
+    Seg s;
+    more = walk.next(s, own_first);
+    s.valid = more;
+    const uint32_t slot = no % kSegRing;
+    if (no >= kSegRing && !mbar_wait(empty + 8u * slot, (no / kSegRing - 1) & 1u, wctx)) return;
+    if ((threadIdx.x & 31) == 0) {
+      ring[slot] = s;
+      mbar_arrive(full + 8u * slot);
+    }
+    __syncwarp();
+  }
+}
+
 // Key tile `t` of a segment: whether it is the prefix's, its first token there and its tokens.
 struct TileInfo {
   bool pre;
   int k0, n;
 };
+template <int KT>
 __device__ __forceinline__ TileInfo tile_info(const PagedParams& p, const Seg& s, int t) {
   TileInfo x;
-  const int lead = s.own && p.packed ? 0 : p.pre_tiles;
-  const int kt = s.own ? p.own_kt : p.pre_kt;
-  x.pre = t < lead;
-  x.k0 = (x.pre ? t : t - lead) << kt;
-  x.n = min(1 << kt, (x.pre ? p.prefix_len : s.visible) - x.k0);
+  x.pre = t < s.lead;
+  x.k0 = (x.pre ? t : t - s.lead) * KT;
+  x.n = min(KT, (x.pre ? p.prefix_len : s.visible) - x.k0);
   return x;
-}
-
-// Where a segment's results go.
-struct Place {
-  bool direct;        // the item is whole and nothing is to be joined
-  long long slot_row; // else: first row of the item's slot
-  int part;
-};
-template <int ITEM>
-__device__ __forceinline__ Place place_of(const PagedParams& p, const Seg& s) {
-  Place x;
-  const bool whole = s.t0 == 0 && s.t1 == s.nt;
-  x.direct = whole && s.own && (!p.packed || p.prefix_len == 0);
-  const long long item = s.own ? ((long long)s.b * p.n_rc + s.rc) * p.H_kv + s.hk
-                               : (long long)s.hk * p.n_groups + s.b / (p.seqs * (ITEM / 128));
-  const long long items = s.own ? (p.packed ? (long long)p.B * p.n_rc * p.H_kv : 0) : (long long)p.n_groups * p.H_kv;
-  x.part = s.own ? p.ctas - 1 - (int)blockIdx.x : (int)blockIdx.x;
-  const long long slot = whole ? item : items + 2 * x.part + (s.t0 == 0 ? 1 : 0);
-  x.slot_row = slot * (s.own ? min(p.R, ITEM) : ITEM);
-  return x;
-}
-// For the joining kernel: which parts of the own line hold the item (by the part that starts it).
-__device__ __forceinline__ void note_parts(const PagedParams& p, const Start& start, const Seg& s, int part) {
-  int last = part;
-  if (s.t1 < s.nt) {  // the item's last unit is nt - t1 units behind this part
-    const int parts = line_parts(p, start.total);
-    last = part_of(start.total, parts, part_begin(start.total, parts, part + 1) + (s.nt - s.t1) - 1);
-  }
-  p.seg[((long long)s.b * p.n_rc + s.rc) * p.H_kv + s.hk] = make_int2(part, last);
 }
 
 // The page of a tile's piece that starts at token `row0` of the tile.
@@ -512,15 +553,14 @@ __device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, 
 // ---------------------------------------------------------------------------- dense form
 // Warps 0 - 3: copies and products.
 template <int D, bool BF>
-__device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedParams& p, const Start& start, bool pre,
-                                            bool own, uint32_t base, uint32_t bars, uint32_t tmem,
-                                           volatile uint32_t* asked_for, const WaitCtx& wctx) {
+__device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedParams& p, SegRing& segs, uint32_t base,
+                                           uint32_t bars, uint32_t tmem, volatile uint32_t* asked_for,
+                                           const WaitCtx& wctx) {
   using L = Dense<D>;
   constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
   constexpr uint32_t NS = L::NS;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Walk<ITEM> walk(p, start, pre, own);
   Seg sg;
 
   if (warp == 0 || warp == 2) {
@@ -534,8 +574,8 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
     uint32_t i = v, issued = 0;  // ring index of the next tile
     int q_count[2] = {0, 0}, region = 0;
     bool ok = true;
-    while (ok && walk.next(sg)) {
-      TileInfo x = tile_info(p, sg, sg.t0);
+    while (ok && segs.next(sg, wctx)) {
+      TileInfo x = tile_info<KT>(p, sg, sg.t0);
       int page = has_box ? look_up(p, sg, x, row0) : 0;
       if (v == 0) {
         // Q: one region for a single tile (the other one keeps the previous item's), both for two tiles
@@ -547,7 +587,7 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
           __syncwarp();
           if (lane < L::KCH)
             tma_load_4d(base + rg * L::QTILE + lane * L::QCHUNK, sg.own ? &maps.q_own : &maps.q_pre, lane * 64,
-                        sg.own ? sg.rc * ITEM + w * 128 : 0, sg.hk, sg.own ? sg.b : sg.b + w * p.seqs,
+                        sg.row0 + w * 128 * sg.own, sg.hk, sg.own ? sg.b : sg.b + w * p.seqs,
                         bar(L::Q_FULL + rg));
           ++q_count[rg];
         }
@@ -558,7 +598,7 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
         const TileInfo y = x;
         const int cur = page;
         if (t + 1 < sg.t1) {
-          x = tile_info(p, sg, t + 1);
+          x = tile_info<KT>(p, sg, t + 1);
           if (has_box) page = look_up(p, sg, x, row0);
         }
         const uint32_t st = i % NS;
@@ -601,7 +641,7 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
           seg_i += 2 * (sg.t1 - sg.t0);
           if (NWG == 2 && !sg.pair) region ^= 1;
         }
-        if (!(more = walk.next(sg))) return f;
+        if (!(more = segs.next(sg, wctx))) return f;
         have = true;
         s = 0;
         n_steps = (sg.t1 - sg.t0) << (sg.pair ? 1 : 0);
@@ -667,17 +707,19 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
 
 // Warps 4 - 11: softmax.
 template <int D, bool BF>
-__device__ __forceinline__ void dense_softmax(const PagedParams& p, const Start& start, bool pre, bool own,
-                                              uint8_t* gbase, uint32_t bars, uint32_t tmem, const WaitCtx& wctx) {
+__device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& segs, uint8_t* gbase, uint32_t bars,
+                                              uint32_t tmem, const WaitCtx& wctx) {
   using L = Dense<D>;
   constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
   constexpr uint32_t NS = L::NS;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = (warp - 4) >> 2;
-  if (w < NWG) {
-    Walk<ITEM> walk(p, start, pre, own);
-    Seg sg;
+  Seg sg;
+  if (w >= NWG) {  // d = 256: one warpgroup only, the other reads along
+    while (segs.next(sg, wctx)) {
+    }
+  } else {
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const uint32_t lanes = (uint32_t)(wq * 32) << 16;
@@ -686,24 +728,21 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, const Start&
     uint32_t kv = 0, total = 0;  // key tiles and steps of earlier segments
     int o_cnt = 0;               // segments that this warpgroup ended
     int stat_cnt = 0;            // statistics handed over (by either warpgroup)
-    while (ok && walk.next(sg)) {
+    while (ok && segs.next(sg, wctx)) {
       const int steps = (sg.t1 - sg.t0) << (sg.pair ? 1 : 0);
       const int s_first = NWG == 2 ? (w ^ (int)(total & 1u)) : 0;
       const int tile_q = sg.pair ? s_first : 0;  // this warpgroup's query tile
       // rows of the tile
-      const int live = sg.own ? min(128, p.R - sg.rc * ITEM - tile_q * 128)
-                              : min(p.seqs, p.B - sg.b - tile_q * p.seqs) * p.R;
+      const int live = tile_q ? sg.rows[1] : sg.rows[0];
       const bool warp_live = wq * 32 < live;
-      bool counts = row < live;  // rows of a sequence that is not there may hold anything
-      if (counts && !sg.own) counts = p.lens[sg.b + tile_q * p.seqs + row / p.R] >= 0;
       int own_lim = sg.visible;
-      if (sg.own && p.causal) own_lim = sg.len - p.T + (sg.rc * ITEM + tile_q * 128 + row) % p.T + 1;
+      if (sg.own && p.causal) own_lim = sg.len - p.T + (sg.row0 + tile_q * 128 + row) % p.T + 1;
       float m = -INFINITY, l = 0.f;
       bool mine = false;
       for (int s = s_first; s < steps; s += NWG) {
         const uint32_t n = total + s, sb = n & 1u;
         const int kt = sg.pair ? s >> 1 : s;
-        const TileInfo x = tile_info(p, sg, sg.t0 + kt);
+        const TileInfo x = tile_info<KT>(p, sg, sg.t0 + kt);
         if (x.n < KT && (!sg.pair || s_first == 0)) {
           // the tile ends behind the last token: rows x.n .. of V are whatever was there before
           const uint32_t i = 2 * (kv + kt) + 1, st = i % NS;
@@ -724,8 +763,11 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, const Start&
                                  });
           if (!ok) break;
           // weights are at most 2^8: a sum that is no finite number came from a non-finite score
-          // (a wrong page may be the reason, and that report stays)
-          if (counts && !(l <= 3.0e38f)) atomicCAS(p.err, kDevOk, kDevRange);
+          // (a wrong page may be the reason, and that report stays), or belongs to the row of a sequence
+          // that is not there, which may hold anything
+          if (row < live && !(l <= 3.0e38f) &&
+              (sg.own || p.lens[sg.b + tile_q * p.seqs + row / p.R] >= 0))
+            atomicCAS(p.err, kDevOk, kDevRange);
         } else {
           for (int h = 0; h < L::HALVES; ++h) mbar_arrive(bar_p + 8u * h);
         }
@@ -759,19 +801,15 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, const Start&
       float ca = M == -INFINITY ? 0.f : ex2_approx(m - M);
       float cb = M == -INFINITY ? 0.f : ex2_approx(theirs.x - M);
       const float sum = ca * l + cb * theirs.y;
-      const Place pl = place_of<ITEM>(p, sg);
-      if (sg.own && sg.t0 == 0 && tile_q == 0 && row == 0) note_parts(p, start, sg, pl.part);
-      if (pl.direct) {
+      if (sg.direct) {
         const float inv = sum > 0.f ? 1.0f / sum : 0.f;
         ca *= inv;
         cb *= inv;
       }
       const bool write = row < live;
-      const long long out_row = ((long long)sg.b * p.H_kv + sg.hk) * p.R + sg.rc * ITEM + tile_q * 128 + row;
-      const long long srow = pl.slot_row + tile_q * 128 + row;
+      const int irow = tile_q * 128 + row;  // row of the item
       const uint32_t tO = tmem + lanes + L::T_O(w), tO2 = tmem + lanes + L::T_O(w ^ 1);
-      uint8_t* dst = pl.direct ? static_cast<uint8_t*>(p.o) + out_row * (2 * D)
-                               : reinterpret_cast<uint8_t*>((sg.own ? p.own_o : p.pre_o) + srow * D);
+      uint8_t* dst = sg.o_dst + (size_t)irow * (sg.direct ? 2 * D : 4 * D);
       if (warp_live) {
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -789,7 +827,7 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, const Start&
 #pragma unroll
             for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(ca * __uint_as_float(u[i]));
           }
-          if (write && pl.direct) {
+          if (write && sg.direct) {
             uint32_t h[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -809,10 +847,10 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, const Start&
       mbar_arrive(bar(L::O_FREE + w));
       if (other) mbar_arrive(bar(L::O_FREE + (w ^ 1)));
       if (write) {
-        if (!pl.direct)
-          (sg.own ? p.own_ml : p.pre_ml)[srow] = make_float2(M, sum);
-        else if (p.lse != nullptr)
-          p.lse[out_row] = log_sum(M, sum);
+        if (!sg.direct)
+          static_cast<float2*>(sg.ml_dst)[irow] = make_float2(M, sum);
+        else if (sg.ml_dst != nullptr)
+          static_cast<float*>(sg.ml_dst)[irow] = log_sum(M, sum);
       }
     }
   }
@@ -841,16 +879,15 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 // A warpgroup's work on one segment with up to N rows (N = 8, 16 or 32): thread k has key k of
 // every tile and, in the end, column k of O.  False (for all threads) if a bounded wait gave up.
 template <int D, bool BF, int N>
-__device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& start, const Seg& sg, uint32_t bars,
+__device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg, uint32_t bars,
                                             uint8_t* gbase, uint32_t tmem, const WaitCtx& wctx, int w, uint32_t kv,
                                             uint32_t seg_no, uint32_t& s_no) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS;
-  constexpr int ITEM = 128 * Dense<D>::NWG;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
   const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, key = wq * 32 + lane;
   const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-  const int rows = sg.own ? p.R : p.R * p.B;
+  const int rows = sg.rows[0];
   const int id = 1 + w;
   float4* ex = reinterpret_cast<float4*>(gbase + L::OFF_EX) + w * 64;  // [2][32]: a value of each warp per row
   uint32_t ex_no = 0;
@@ -866,7 +903,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
   const int n_tiles = sg.t1 - sg.t0;
   for (int t = 0; t < n_tiles; ++t, ++s_no) {
     const uint32_t n = kv + t;  // step of the phase
-    const TileInfo x = tile_info(p, sg, sg.t0 + t);
+    const TileInfo x = tile_info<128>(p, sg, sg.t0 + t);
     ok &= mbar_wait(bar(L::S_FULL + 2 * w + (s_no & 1u)), s_no / 2 & 1u, wctx);
     tc_fence_after();
     float s[N];
@@ -969,17 +1006,14 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
       total[r] = (q.x + q.y) + (q.z + q.w);
     }
   }
-  const Place pl = place_of<ITEM>(p, sg);
-  if (sg.own && sg.t0 == 0 && key == 0) note_parts(p, start, sg, pl.part);
-  const long long out_row = ((long long)sg.b * p.H_kv + sg.hk) * p.R;  // own items
 #pragma unroll
   for (int r = 0; r < N; ++r)
     if (key == r && r < rows) {
       if (!(total[r] <= 3.0e38f) && (sg.own || p.lens[r / p.R] >= 0)) atomicCAS(p.err, kDevOk, kDevRange);
-      if (!pl.direct)
-        (sg.own ? p.own_ml : p.pre_ml)[pl.slot_row + r] = make_float2(m[r], total[r]);
-      else if (p.lse != nullptr)
-        p.lse[out_row + r] = log_sum(m[r], total[r]);
+      if (!sg.direct)
+        static_cast<float2*>(sg.ml_dst)[r] = make_float2(m[r], total[r]);
+      else if (sg.ml_dst != nullptr)
+        static_cast<float*>(sg.ml_dst)[r] = log_sum(m[r], total[r]);
     }
   ok &= mbar_wait(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
   tc_fence_after();
@@ -997,11 +1031,11 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
         if (r >= rows) continue;
         const float v = __uint_as_float(u[h][r]);
         const int col = h * 128 + key;
-        if (pl.direct)
-          static_cast<uint16_t*>(p.o)[(out_row + r) * D + col] =
+        if (sg.direct)
+          reinterpret_cast<uint16_t*>(sg.o_dst)[r * D + col] =
               round16<BF>(total[r] > 0.f ? v * __frcp_rn(total[r]) : 0.f);
         else
-          (sg.own ? p.own_o : p.pre_o)[(pl.slot_row + r) * D + col] = v;
+          reinterpret_cast<float*>(sg.o_dst)[r * D + col] = v;
       }
   }
   return !group_any(id, !ok);
@@ -1009,15 +1043,14 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Start& s
 
 // Warps 0 - 3: copies and products.
 template <int D, bool BF>
-__device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParams& p, const Start& start, bool pre,
-                                          bool own, uint32_t base, uint32_t bars, uint32_t tmem,
-                                         volatile uint32_t* asked_for, const WaitCtx& wctx) {
+__device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParams& p, SegRing& segs, uint32_t base,
+                                         uint32_t bars, uint32_t tmem, volatile uint32_t* asked_for,
+                                         const WaitCtx& wctx) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS, NQ = L::NQ;
-  constexpr int PARTS = L::PARTS, ITEM = 128 * Dense<D>::NWG;
+  constexpr int PARTS = L::PARTS;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Walk<ITEM> walk(p, start, pre, own);
   Seg sg;
 
   if (warp == 0 || warp == 2) {
@@ -1031,13 +1064,13 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
     uint32_t i = v * PARTS, seg_no = 0;  // ring index of the next tile
     uint32_t issued = 0;                 // ring index behind the last slot asked for
     bool ok = true;
-    for (; ok && walk.next(sg); ++seg_no) {
-      TileInfo x = tile_info(p, sg, sg.t0);
+    for (; ok && segs.next(sg, wctx); ++seg_no) {
+      TileInfo x = tile_info<128>(p, sg, sg.t0);
       int page = has_box ? look_up(p, sg, x, row0) : 0;
       if (v == 0) {
         const uint32_t qb = seg_no % NQ;
         if (seg_no >= NQ && !(ok = mbar_wait(bar(L::Q_EMPTY + qb), (seg_no / NQ - 1) & 1u, wctx))) break;
-        const int rows = sg.own ? p.R : p.R * p.B;
+        const int rows = sg.rows[0];
         if (lane == 0) mbar_arrive_expect_tx(bar(L::Q_FULL + qb), (uint32_t)rows * 128u * L::KCH);
         __syncwarp();
         if (lane < L::KCH)
@@ -1048,7 +1081,7 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
         const TileInfo y = x;
         const int cur = page;
         if (t + 1 < sg.t1) {
-          x = tile_info(p, sg, t + 1);
+          x = tile_info<128>(p, sg, t + 1);
           if (has_box) page = look_up(p, sg, x, row0);
         }
         const uint32_t bytes = (uint32_t)((y.n + p.box_rows - 1) / p.box_rows) * p.box_rows * 128u * L::PCH;
@@ -1092,11 +1125,11 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
       Step f{};
       if (!more) return f;
       if (t == n_tiles) {
-        if (!(more = walk.next(sg))) return f;
+        if (!(more = segs.next(sg, wctx))) return f;
         ++seg_no;
         t = 0;
         n_tiles = sg.t1 - sg.t0;
-        cols = (sg.own ? p.R : p.R * p.B) <= 16 ? 16 : 32;
+        cols = sg.rows[0] <= 16 ? 16 : 32;
       }
       const uint32_t qb = seg_no % NQ;
       if (t == 0 && !(ok = mbar_wait(bar(L::Q_FULL + qb), seg_no / NQ & 1u, wctx))) return f;
@@ -1158,18 +1191,17 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
 
 // Warps 4 - 11: softmax, the two warpgroups take segments in turn.
 template <int D, bool BF>
-__device__ __forceinline__ void few_softmax(const PagedParams& p, const Start& start, bool pre, bool own, uint8_t* gbase,
-                                            uint32_t bars, uint32_t tmem, const WaitCtx& wctx) {
-  Walk<128 * Dense<D>::NWG> walk(p, start, pre, own);
+__device__ __forceinline__ void few_softmax(const PagedParams& p, SegRing& segs, uint8_t* gbase, uint32_t bars,
+                                            uint32_t tmem, const WaitCtx& wctx) {
   Seg sg;
   const int w = (int)(threadIdx.x >> 7) - 1;
   uint32_t kv = 0, seg_no = 0, s_no = 0;
-  for (; walk.next(sg); kv += sg.t1 - sg.t0, ++seg_no) {
+  for (; segs.next(sg, wctx); kv += sg.t1 - sg.t0, ++seg_no) {
     if ((seg_no & 1u) != (uint32_t)w) continue;
-    const int rows = sg.own ? p.R : p.R * p.B;
-    const bool ok = rows <= 8    ? few_segment<D, BF, 8>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
-                    : rows <= 16 ? few_segment<D, BF, 16>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
-                                 : few_segment<D, BF, 32>(p, start, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no);
+    const int rows = sg.rows[0];
+    const bool ok = rows <= 8    ? few_segment<D, BF, 8>(p, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                    : rows <= 16 ? few_segment<D, BF, 16>(p, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                                 : few_segment<D, BF, 32>(p, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no);
     if (!ok) break;
   }
 }
@@ -1190,15 +1222,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Start& start = *reinterpret_cast<Start*>(gbase + M::OFF_START);
 
-  if (threadIdx.x < Dense<D>::NBAR + Few<D>::NBAR) {
-    // arrivals: the 128 threads of a warpgroup where P, O or statistics are handed over, else 1
+  if (threadIdx.x < M::NBAR) {
+    // arrivals: the 128 threads of a warpgroup where P, O or statistics are handed over, the reading
+    // warps of a segment, else 1
     const int i = threadIdx.x, f = i - Dense<D>::NBAR;
     using A = Dense<D>;
     using F = Few<D>;
     const bool group = f < 0 ? (i >= A::P_FULL && i < A::P_FULL + 4) || (i >= A::O_FREE && i < A::O_FREE + 2) ||
                                    i == A::STAT_FULL || i == A::STAT_EMPTY
                              : (f >= F::P_FULL && f < F::P_FULL + 2) || (f >= F::O_FREE && f < F::O_FREE + 2);
-    mbar_init(bars + 8u * i, group ? 128 : 1);
+    const bool in_few = f < F::NBAR;
+    mbar_init(bars + 8u * i, i >= M::SEG_EMPTY ? kSegReaders : group && in_few ? 128 : 1);
     fence_barrier_init();
   }
   if (threadIdx.x == 0) {
@@ -1286,27 +1320,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     return false;
   };
+  Seg* ring = reinterpret_cast<Seg*>(gbase + M::OFF_SEG);
+  SegRing segs{ring, bars + 8u * M::SEG_FULL, bars + 8u * M::SEG_EMPTY, 0};
   if (warp < 4) {
     regs_dec<kRegsLow>();
 #pragma unroll 1
     for (int phase = 0; phase < phases; ++phase) {
       const bool do_own = both || (phase == 0) == own_first, do_pre = pre && (both || !do_own);
-      if (do_own ? p.own_few : p.pre_few)
-        few_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::FEW_BAR, tmem, asked_for, wctx);
+      const bool few = do_own ? p.own_few : p.pre_few;
+      if (warp == 3)
+        schedule<D>(p, start, do_pre, do_own, own_first, ring, segs.full, segs.empty, segs.no, wctx);
+      else if (few)
+        few_feed<D, BF>(maps, p, segs, base, bars + 8u * M::FEW_BAR, tmem, asked_for, wctx);
       else
-        dense_feed<D, BF>(maps, p, start, do_pre, do_own, base, bars + 8u * M::DENSE_BAR, tmem, asked_for, wctx);
-      if (!phase_end(do_own ? p.own_few : p.pre_few)) break;
+        dense_feed<D, BF>(maps, p, segs, base, bars + 8u * M::DENSE_BAR, tmem, asked_for, wctx);
+      if (!phase_end(few)) break;
     }
   } else {
     regs_inc<kRegsHigh>();
 #pragma unroll 1
     for (int phase = 0; phase < phases; ++phase) {
-      const bool do_own = both || (phase == 0) == own_first, do_pre = pre && (both || !do_own);
-      if (do_own ? p.own_few : p.pre_few)
-        few_softmax<D, BF>(p, start, do_pre, do_own, gbase, bars + 8u * M::FEW_BAR, tmem, wctx);
+      const bool do_own = both || (phase == 0) == own_first;
+      const bool few = do_own ? p.own_few : p.pre_few;
+      if (few)
+        few_softmax<D, BF>(p, segs, gbase, bars + 8u * M::FEW_BAR, tmem, wctx);
       else
-        dense_softmax<D, BF>(p, start, do_pre, do_own, gbase, bars + 8u * M::DENSE_BAR, tmem, wctx);
-      if (!phase_end(do_own ? p.own_few : p.pre_few)) break;
+        dense_softmax<D, BF>(p, segs, gbase, bars + 8u * M::DENSE_BAR, tmem, wctx);
+      if (!phase_end(few)) break;
     }
   }
   if (warp == 1) tmem_dealloc(tmem, 512);
