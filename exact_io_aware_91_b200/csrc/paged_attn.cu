@@ -199,11 +199,6 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) 
     tmem_st8(taddr, r);
 }
 
-__device__ __forceinline__ float warp_max(float x) {  // over the 32 lanes
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Whether any of the 128 threads of a warpgroup says so; a barrier among them as well.
 __device__ __forceinline__ bool group_any(int id, bool x) {
   uint32_t r;
@@ -857,10 +852,10 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
 }
 
 // ---------------------------------------------------------------------------- few rows: softmax
-// Sums of v[r] over the 32 lanes for all r at once: halves of the rows go to halves of the lanes, so
-// N values cost N - 1 exchanges (and log2(32 / N) more); lane l ends with the sum of row l % N.
-template <int N>
-__device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
+// v[r] joined over the 32 lanes by `op`, for all r at once: halves of the rows go to halves of the
+// lanes, so N values cost N - 1 exchanges (and log2(32 / N) more); lane l ends with row l % N.
+template <int N, class Op>
+__device__ __forceinline__ float warp_join(const float (&v)[N], int lane, Op op) {
   if constexpr (N > 1) {
     constexpr int H = N / 2;
     const bool up = (lane & H) != 0;
@@ -868,12 +863,23 @@ __device__ __forceinline__ float warp_sums(float (&v)[N], int lane) {
 #pragma unroll
     for (int i = 0; i < H; ++i) {
       const float send = up ? v[i] : v[i + H], keep = up ? v[i + H] : v[i];
-      w[i] = keep + __shfl_xor_sync(0xffffffffu, send, H);
+      w[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, H));
     }
-    return warp_sums<H>(w, lane);
+    return warp_join<H>(w, lane, op);
   } else {
     return v[0];
   }
+}
+// The same over the 128 threads of a warpgroup, through `ex` (a value of each warp per row).
+template <int N, class Op>
+__device__ __forceinline__ float group_join(const float (&v)[N], int lane, int wq, int id, float4* ex, Op op) {
+  float x = warp_join<N>(v, lane, op);
+#pragma unroll
+  for (int d = N; d < 32; d <<= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, d));
+  if (lane < N) reinterpret_cast<float*>(ex + lane)[wq] = x;
+  group_sync(id);
+  const float4 q = ex[lane % N];
+  return op(op(q.x, q.y), op(q.z, q.w));
 }
 
 // A warpgroup's work on one segment with up to N rows (N = 8, 16 or 32): thread k has key k of
@@ -891,7 +897,13 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   const int id = 1 + w;
   float4* ex = reinterpret_cast<float4*>(gbase + L::OFF_EX) + w * 64;  // [2][32]: a value of each warp per row
   uint32_t ex_no = 0;
+  const auto fmax_op = [](float a, float b) { return fmaxf(a, b); };
+  const auto sum_op = [](float a, float b) { return a + b; };
+  // Rows are spread over registers where every key needs them (m, l) and over lanes where one value per
+  // row is wanted: code that runs once per segment has to be short, it comes from far.  Rows behind
+  // the last one compute along with whatever Q's buffer holds there; nothing reads them.
   float m[N], l[N];
+  float m_lane = -INFINITY;  // of row lane % N
 #pragma unroll
   for (int r = 0; r < N; ++r) {
     m[r] = -INFINITY;
@@ -901,6 +913,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   // barriers among the warpgroup need all of its threads.
   bool ok = true;
   const int n_tiles = sg.t1 - sg.t0;
+#pragma unroll 1
   for (int t = 0; t < n_tiles; ++t, ++s_no) {
     const uint32_t n = kv + t;  // step of the phase
     const TileInfo x = tile_info<128>(p, sg, sg.t0 + t);
@@ -914,55 +927,50 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
 #pragma unroll
       for (int r = 0; r < N; ++r) s[r] = __uint_as_float(u[r]) * p.scale_log2;
     }
-    // masks: rows that are not there, and keys that a row does not see.  All rows of a prefix
-    // tile, and all of a sequence's with one token each, see the same keys.
-    const bool steps_in = !x.pre && p.causal && p.T > 1;  // rows differ
-    const int first_lim = steps_in ? sg.len - p.T + 1 - x.k0 : x.n;
-    if (rows < N || first_lim < 128) {
-      int tok = 0;
+    // keys that a row does not see; all rows see the same ones, except own keys with several causal tokens
+    if (!x.pre && p.causal && p.T > 1) {
+      const int lim0 = sg.len - p.T + 1 - x.k0;  // of the first token
+      if (lim0 < 128) {
+        int tok = 0;
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        if (r >= rows || key >= min(x.n, first_lim + tok)) s[r] = -INFINITY;
-        if (steps_in && ++tok == p.T) tok = 0;
+        for (int r = 0; r < N; ++r) {
+          if (key >= lim0 + tok) s[r] = -INFINITY;
+          if (++tok == p.T) tok = 0;
+        }
       }
+    } else if (key >= x.n) {
+#pragma unroll
+      for (int r = 0; r < N; ++r) s[r] = -INFINITY;
     }
     bool above = false;
 #pragma unroll
     for (int r = 0; r < N; ++r) above |= s[r] > m[r] + 8.0f;
     if (group_any(id, above)) {
       // a maximum has moved by 2^8 or more (always on the first tile): take the tile's maxima
-      float mine = -INFINITY;
+      const float t_max = group_join<N>(s, lane, wq, id, ex + (ex_no++ & 1u) * 32, fmax_op);
+      const float m_new = fmaxf(m_lane, t_max);
+      const float m_use = (m_new - m_lane > 8.0f) ? m_new : m_lane;
+      const float alpha = m_use == m_lane ? 1.0f : ex2_approx(m_lane - m_use);
+      m_lane = m_use;
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const float t_max = warp_max(s[r]);
-        if (lane == r) mine = t_max;
-      }
-      float4* e = ex + (ex_no++ & 1u) * 32;
-      if (lane < N) reinterpret_cast<float*>(e + lane)[wq] = mine;
-      group_sync(id);
-      float alpha[N];
-      bool moved = false;
-#pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const float4 v = e[r];
-        const float m_new = fmaxf(m[r], fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-        const float m_use = (m_new - m[r] > 8.0f) ? m_new : m[r];
-        alpha[r] = m_use == m[r] ? 1.0f : ex2_approx(m[r] - m_use);
-        moved |= alpha[r] != 1.0f;
-        m[r] = m_use;
-        l[r] *= alpha[r];
-      }
-      if (moved && t > 0) {  // (the same for all threads)
+      for (int r = 0; r < N; ++r) m[r] = __shfl_sync(0xffffffffu, m_use, r);
+      if (t > 0) {
         // O^T holds the earlier tiles once their products have completed
         ok &= mbar_wait(bar(L::P_EMPTY + ((n - 1) & 1u)), (n - 1) / 2 & 1u, wctx);
         tc_fence_after();
+        float a[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+          a[r] = __shfl_sync(0xffffffffu, alpha, r);
+          l[r] *= a[r];
+        }
 #pragma unroll
         for (int h = 0; h < L::PARTS; ++h) {
           uint32_t u[N];
           tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u);
           tmem_wait_ld();
 #pragma unroll
-          for (int r = 0; r < N; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * alpha[r]);
+          for (int r = 0; r < N; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * a[r]);
           tmem_st<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u);
         }
         tmem_wait_st();
@@ -992,29 +1000,16 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
     mbar_arrive(bar(L::P_FULL + (n & 1u)));
   }
   // ---- the end of the segment: row sums over the threads, then column `key` of each row
-  float total[N];
-  {
-    float v = warp_sums<N>(l, lane);
-#pragma unroll
-    for (int d = N; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    float4* e = ex + (ex_no++ & 1u) * 32;
-    if (lane < N) reinterpret_cast<float*>(e + lane)[wq] = v;
-    group_sync(id);
-#pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float4 q = e[r];
-      total[r] = (q.x + q.y) + (q.z + q.w);
-    }
+  const float total = group_join<N>(l, lane, wq, id, ex + (ex_no++ & 1u) * 32, sum_op);  // of row lane % N
+  float factor = 1.0f;
+  if (sg.direct) factor = total > 0.f ? 1.0f / total : 0.f;
+  if (key < rows) {  // (warp 0)
+    if (!(total <= 3.0e38f) && (sg.own || p.lens[key / p.R] >= 0)) atomicCAS(p.err, kDevOk, kDevRange);
+    if (!sg.direct)
+      static_cast<float2*>(sg.ml_dst)[key] = make_float2(m_lane, total);
+    else if (sg.ml_dst != nullptr)
+      static_cast<float*>(sg.ml_dst)[key] = log_sum(m_lane, total);
   }
-#pragma unroll
-  for (int r = 0; r < N; ++r)
-    if (key == r && r < rows) {
-      if (!(total[r] <= 3.0e38f) && (sg.own || p.lens[r / p.R] >= 0)) atomicCAS(p.err, kDevOk, kDevRange);
-      if (!sg.direct)
-        static_cast<float2*>(sg.ml_dst)[r] = make_float2(m[r], total[r]);
-      else if (sg.ml_dst != nullptr)
-        static_cast<float*>(sg.ml_dst)[r] = log_sum(m[r], total[r]);
-    }
   ok &= mbar_wait(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
   tc_fence_after();
   uint32_t u[L::PARTS][N];
@@ -1023,20 +1018,24 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   tmem_wait_ld();
   tc_fence_before();
   mbar_arrive(bar(L::O_FREE + (seg_no & 1u)));
-  if (D >= 128 || key < D) {
+  const bool write = D >= 128 || key < D;
+  const int esize = sg.direct ? 2 : 4;
+  uint8_t* dst = sg.o_dst + key * esize;
 #pragma unroll
-    for (int h = 0; h < L::PARTS; ++h)
+  for (int r = 0; r < N; ++r) {
+    const float f = __shfl_sync(0xffffffffu, factor, r);
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        if (r >= rows) continue;
-        const float v = __uint_as_float(u[h][r]);
-        const int col = h * 128 + key;
+    for (int h = 0; h < L::PARTS; ++h) {
+      const float v = __uint_as_float(u[h][r]) * f;
+      uint8_t* at = dst + h * 128 * esize;
+      if (write && r < rows) {
         if (sg.direct)
-          reinterpret_cast<uint16_t*>(sg.o_dst)[r * D + col] =
-              round16<BF>(total[r] > 0.f ? v * __frcp_rn(total[r]) : 0.f);
+          *reinterpret_cast<uint16_t*>(at) = round16<BF>(v);
         else
-          reinterpret_cast<float*>(sg.o_dst)[r * D + col] = v;
+          *reinterpret_cast<float*>(at) = v;
       }
+    }
+    dst += D * esize;
   }
   return !group_any(id, !ok);
 }
