@@ -138,6 +138,41 @@ struct Smem {
   static_assert(ALLOC <= 232448, "shared memory per CTA");
 };
 
+// mbar_wait in as few instructions as it takes (the segments' code competes for the instruction
+// cache): the same limit, on the low word of the timer, and an abort flag; the end of the phase puts
+// that into the error word.
+struct Waits {
+  uint32_t abort_flag;  // shared memory address
+};
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Waits& w) {
+  static_assert(kWaitLimitNs < (1ull << 32), "the limit fits the timer's low word");
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 t0, t1;\n\t"
+      "mov.u32 %0, 1;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u32 t0, %globaltimer_lo;\n\t"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "ld.volatile.shared::cta.u32 t1, [%3];\n\t"
+      "setp.ne.u32 p, t1, 0;\n\t"
+      "@p bra FAIL;\n\t"
+      "mov.u32 t1, %globaltimer_lo;\n\t"
+      "sub.u32 t1, t1, t0;\n\t"
+      "setp.lt.u32 p, t1, %4;\n\t"
+      "@p bra AGAIN;\n\t"
+      "st.volatile.shared::cta.u32 [%3], 1;\n\t"
+      "FAIL:\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "DONE:\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(w.abort_flag), "n"((uint32_t)kWaitLimitNs)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
@@ -171,10 +206,10 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// N = 8, 16 or 32 consecutive columns of this warp's 32 lanes.
+// N = 4, 8, 16 or 32 consecutive columns of this warp's 32 lanes.
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16 || N == 32, "column counts in use");
+  static_assert(N == 4 || N == 8 || N == 16 || N == 32, "column counts in use");
   if constexpr (N == 32) {
     tmem_ld32(taddr, r);
   } else if constexpr (N == 16) {
@@ -183,6 +218,10 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
+  } else if constexpr (N == 4) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
   } else {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -195,8 +234,12 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) 
     tmem_st32(taddr, r);
   else if constexpr (N == 16)
     tmem_st16(taddr, r);
-  else
+  else if constexpr (N == 8)
     tmem_st8(taddr, r);
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 // Whether any of the 128 threads of a warpgroup says so; a barrier among them as well.
@@ -218,6 +261,10 @@ __device__ __forceinline__ void st_global_32b(void* dst, const uint32_t* v) {  /
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t x) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(x) : "memory");
 }
 
 template <bool BF>
@@ -405,9 +452,9 @@ struct SegRing {
   const Seg* ring;
   uint32_t full, empty;  // barriers
   uint32_t no;
-  __device__ __forceinline__ bool next(Seg& s, const WaitCtx& wctx) {
+  __device__ __forceinline__ bool next(Seg& s, const Waits& wctx) {
     const uint32_t slot = no % kSegRing;
-    if (!mbar_wait(full + 8u * slot, no / kSegRing & 1u, wctx)) return false;
+    if (!wait_bar(full + 8u * slot, no / kSegRing & 1u, wctx)) return false;
     s = ring[slot];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8u * slot);
@@ -418,14 +465,14 @@ struct SegRing {
 // Warp 3: the segments of a phase, and one that says that there are no more.
 template <int D>
 __device__ __forceinline__ void schedule(const PagedParams& p, const Start& start, bool pre, bool own, bool own_first,
-                                         Seg* ring, uint32_t full, uint32_t empty, uint32_t& no, const WaitCtx& wctx) {
+                                         Seg* ring, uint32_t full, uint32_t empty, uint32_t& no, const Waits& wctx) {
   Walk<D> walk(p, start, pre, own);
   for (bool more = true; more; ++no) {
     Seg s;
     more = walk.next(s, own_first);
     s.valid = more;
     const uint32_t slot = no % kSegRing;
-    if (no >= kSegRing && !mbar_wait(empty + 8u * slot, (no / kSegRing - 1) & 1u, wctx)) return;
+    if (no >= kSegRing && !wait_bar(empty + 8u * slot, (no / kSegRing - 1) & 1u, wctx)) return;
     if ((threadIdx.x & 31) == 0) {
       ring[slot] = s;
       mbar_arrive(full + 8u * slot);
@@ -463,7 +510,9 @@ __device__ __forceinline__ int look_up(const PagedParams& p, const Seg& s, const
 // 16-byte units inside a row, does not matter), by the 128 threads of a warpgroup.
 __device__ __forceinline__ void zero_rows(uint8_t* slot, int chunks, int chunk_bytes, int n) {
   const int units = (chunk_bytes - n * 128) / 16;
+#pragma unroll 1
   for (int c = 0; c < chunks; ++c)
+#pragma unroll 1
     for (int z = (int)threadIdx.x & 127; z < units; z += 128)
       *reinterpret_cast<uint4*>(slot + c * chunk_bytes + n * 128 + z * 16) = make_uint4(0, 0, 0, 0);
 }
@@ -550,7 +599,7 @@ __device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, 
 template <int D, bool BF>
 __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedParams& p, SegRing& segs, uint32_t base,
                                            uint32_t bars, uint32_t tmem, volatile uint32_t* asked_for,
-                                           const WaitCtx& wctx) {
+                                           const Waits& wctx) {
   using L = Dense<D>;
   constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
   constexpr uint32_t NS = L::NS;
@@ -576,7 +625,7 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
         // Q: one region for a single tile (the other one keeps the previous item's), both for two tiles
         for (int w = 0; w < (sg.pair ? 2 : 1); ++w) {
           const int rg = sg.pair ? w : region;
-          if (q_count[rg] > 0 && !(ok = mbar_wait(bar(L::Q_EMPTY + rg), (q_count[rg] - 1) & 1, wctx))) break;
+          if (q_count[rg] > 0 && !(ok = wait_bar(bar(L::Q_EMPTY + rg), (q_count[rg] - 1) & 1, wctx))) break;
           const int rows = min(p.R, 128) * (sg.own ? 1 : p.seqs);
           if (lane == 0) mbar_arrive_expect_tx(bar(L::Q_FULL + rg), (uint32_t)rows * 128u * L::KCH);
           __syncwarp();
@@ -597,7 +646,7 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
           if (has_box) page = look_up(p, sg, x, row0);
         }
         const uint32_t st = i % NS;
-        if (!(ok = mbar_wait(bar(L::KV_EMPTY + st), (i / NS & 1u) ^ 1u, wctx))) break;
+        if (!(ok = wait_bar(bar(L::KV_EMPTY + st), (i / NS & 1u) ^ 1u, wctx))) break;
         const uint32_t boxes = (y.n + p.box_rows - 1) / p.box_rows;
         if (lane == 0) mbar_arrive_expect_tx(bar(L::KV_FULL + st), boxes * p.box_rows * 128u * L::KCH);
         __syncwarp();
@@ -645,10 +694,10 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
       const int rg = sg.pair ? q : region, per = sg.pair ? 2 : 1;
       const uint32_t i = seg_i + 2u * (uint32_t)(sg.pair ? s >> 1 : s), st = i % NS, sb = s_total & 1u;
       if (s < per) {
-        if (!(ok = mbar_wait(bar(L::Q_FULL + rg), q_use[rg] & 1, wctx))) return f;
+        if (!(ok = wait_bar(bar(L::Q_FULL + rg), q_use[rg] & 1, wctx))) return f;
         ++q_use[rg];
       }
-      if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) return f;
+      if (!(ok = wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx))) return f;
       tc_fence_after();
       const uint64_t dq = sdesc_add(dQ0, rg * L::QTILE), dk = sdesc_add(dK0, st * L::SLOT);
 #pragma unroll
@@ -674,14 +723,14 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
     for (uint32_t total = 0; ok && f0.valid; ++total) {
       const uint32_t sb = total & 1u, w = NWG == 2 ? sb : 0, st = f0.i % NS;
       if (f0.first) {  // the accumulator's last results have been read
-        if (o_use[w] > 0 && !(ok = mbar_wait(bar(L::O_FREE + w), (o_use[w] - 1) & 1, wctx))) break;
+        if (o_use[w] > 0 && !(ok = wait_bar(bar(L::O_FREE + w), (o_use[w] - 1) & 1, wctx))) break;
         ++o_use[w];
       }
-      if (!(ok = mbar_wait(bar(L::KV_FULL + st), f0.i / NS & 1u, wctx))) break;
+      if (!(ok = wait_bar(bar(L::KV_FULL + st), f0.i / NS & 1u, wctx))) break;
       const uint64_t dv = sdesc_add(dV0, st * L::SLOT);
 #pragma unroll
       for (int h = 0; h < L::HALVES; ++h) {
-        if (!(ok = mbar_wait(bar(L::P_FULL + 2 * sb + h), total / 2 & 1u, wctx))) break;
+        if (!(ok = wait_bar(bar(L::P_FULL + 2 * sb + h), total / 2 & 1u, wctx))) break;
         tc_fence_after();
 #pragma unroll
         for (int k = 4 * h; k < 4 * h + 4; ++k)
@@ -703,7 +752,7 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
 // Warps 4 - 11: softmax.
 template <int D, bool BF>
 __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& segs, uint8_t* gbase, uint32_t bars,
-                                              uint32_t tmem, const WaitCtx& wctx) {
+                                              uint32_t tmem, const Waits& wctx) {
   using L = Dense<D>;
   constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
   constexpr uint32_t NS = L::NS;
@@ -741,11 +790,11 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
         if (x.n < KT && (!sg.pair || s_first == 0)) {
           // the tile ends behind the last token: rows x.n .. of V are whatever was there before
           const uint32_t i = 2 * (kv + kt) + 1, st = i % NS;
-          if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) break;
+          if (!(ok = wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx))) break;
           zero_rows(gbase + L::OFF_KV + st * L::SLOT, L::KCH, L::CHUNK, x.n);
           fence_proxy_async_smem();
         }
-        if (!(ok = mbar_wait(bar(L::S_FULL + sb), n / 2 & 1u, wctx))) break;
+        if (!(ok = wait_bar(bar(L::S_FULL + sb), n / 2 & 1u, wctx))) break;
         tc_fence_after();
         const uint32_t bar_p = bar(L::P_FULL + 2 * sb);
         if (warp_live) {
@@ -753,7 +802,7 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
           ok = dense_step<D, BF>(tmem + lanes + L::T_S(sb), tmem + lanes + L::T_O(w), p.scale_log2, lim, !mine, m, l,
                                  bar_p, [&]() -> bool {
                                    // one accumulator: the previous step's product may still run
-                                   if constexpr (NWG == 1) return mbar_wait(bar(L::PV_DONE), (n - 1) & 1u, wctx);
+                                   if constexpr (NWG == 1) return wait_bar(bar(L::PV_DONE), (n - 1) & 1u, wctx);
                                    return true;
                                  });
           if (!ok) break;
@@ -778,18 +827,18 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
       float2 theirs = make_float2(-INFINITY, 0.f);
       if (other) {
         if (((total - 1) & 1u) != (uint32_t)w) {
-          if (stat_cnt > 0 && !(ok = mbar_wait(bar(L::STAT_EMPTY), (stat_cnt - 1) & 1, wctx))) break;
+          if (stat_cnt > 0 && !(ok = wait_bar(bar(L::STAT_EMPTY), (stat_cnt - 1) & 1, wctx))) break;
           stat[row] = make_float2(m, l);
           mbar_arrive(bar(L::STAT_FULL));
           ++stat_cnt;
           continue;
         }
-        if (!(ok = mbar_wait(bar(L::STAT_FULL), stat_cnt & 1, wctx))) break;
+        if (!(ok = wait_bar(bar(L::STAT_FULL), stat_cnt & 1, wctx))) break;
         ++stat_cnt;
         theirs = stat[row];
         mbar_arrive(bar(L::STAT_EMPTY));
       }
-      if (!(ok = mbar_wait(bar(L::O_FULL + w), o_cnt & 1, wctx))) break;
+      if (!(ok = wait_bar(bar(L::O_FULL + w), o_cnt & 1, wctx))) break;
       ++o_cnt;
       tc_fence_after();
       const float M = fmaxf(m, theirs.x);
@@ -882,11 +931,11 @@ __device__ __forceinline__ float group_join(const float (&v)[N], int lane, int w
   return op(op(q.x, q.y), op(q.z, q.w));
 }
 
-// A warpgroup's work on one segment with up to N rows (N = 8, 16 or 32): thread k has key k of
+// A warpgroup's work on one segment with up to N rows (N = 4, 8, 16 or 32): thread k has key k of
 // every tile and, in the end, column k of O.  False (for all threads) if a bounded wait gave up.
 template <int D, bool BF, int N>
 __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg, uint32_t bars,
-                                            uint8_t* gbase, uint32_t tmem, const WaitCtx& wctx, int w, uint32_t kv,
+                                            uint32_t base, uint8_t* gbase, uint32_t tmem, const Waits& wctx, int w, uint32_t kv,
                                             uint32_t seg_no, uint32_t& s_no) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS;
@@ -902,11 +951,15 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   // Rows are spread over registers where every key needs them (m, l) and over lanes where one value per
   // row is wanted: code that runs once per segment has to be short, it comes from far.  Rows behind
   // the last one compute along with whatever Q's buffer holds there; nothing reads them.
-  float m[N], l[N];
-  float m_lane = -INFINITY;  // of row lane % N
+  // Maxima are those of the unscaled scores: a weight is 2^(scale s + shift), shift = -scale max, and the
+  // maximum has moved by 2^8 once s > limit = max + 8 / scale.
+  const float sl2 = p.scale_log2, lag = fminf(8.0f / sl2, 1e30f);
+  float shift[N], limit[N], l[N];
+  float m_lane = -INFINITY;  // maximum of row lane % N
 #pragma unroll
   for (int r = 0; r < N; ++r) {
-    m[r] = -INFINITY;
+    shift[r] = 0.f;
+    limit[r] = -INFINITY;
     l[r] = 0.f;
   }
   // A wait that gave up leaves ok false, and the segment goes on to its end all the same: the
@@ -917,7 +970,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   for (int t = 0; t < n_tiles; ++t, ++s_no) {
     const uint32_t n = kv + t;  // step of the phase
     const TileInfo x = tile_info<128>(p, sg, sg.t0 + t);
-    ok &= mbar_wait(bar(L::S_FULL + 2 * w + (s_no & 1u)), s_no / 2 & 1u, wctx);
+    ok &= wait_bar(bar(L::S_FULL + 2 * w + (s_no & 1u)), s_no / 2 & 1u, wctx);
     tc_fence_after();
     float s[N];
     {
@@ -925,7 +978,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
       tmem_ld<N>(tmem + lanes + L::T_S(n & 3u), u);
       tmem_wait_ld();
 #pragma unroll
-      for (int r = 0; r < N; ++r) s[r] = __uint_as_float(u[r]) * p.scale_log2;
+      for (int r = 0; r < N; ++r) s[r] = __uint_as_float(u[r]);
     }
     // keys that a row does not see; all rows see the same ones, except own keys with several causal tokens
     if (!x.pre && p.causal && p.T > 1) {
@@ -944,19 +997,23 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
     }
     bool above = false;
 #pragma unroll
-    for (int r = 0; r < N; ++r) above |= s[r] > m[r] + 8.0f;
+    for (int r = 0; r < N; ++r) above |= s[r] > limit[r];
     if (group_any(id, above)) {
       // a maximum has moved by 2^8 or more (always on the first tile): take the tile's maxima
       const float t_max = group_join<N>(s, lane, wq, id, ex + (ex_no++ & 1u) * 32, fmax_op);
       const float m_new = fmaxf(m_lane, t_max);
-      const float m_use = (m_new - m_lane > 8.0f) ? m_new : m_lane;
-      const float alpha = m_use == m_lane ? 1.0f : ex2_approx(m_lane - m_use);
+      const float m_use = m_new > m_lane + lag ? m_new : m_lane;
+      const float alpha = m_use == m_lane ? 1.0f : ex2_approx((m_lane - m_use) * sl2);
       m_lane = m_use;
 #pragma unroll
-      for (int r = 0; r < N; ++r) m[r] = __shfl_sync(0xffffffffu, m_use, r);
+      for (int r = 0; r < N; ++r) {
+        const float x_r = __shfl_sync(0xffffffffu, m_use, r);
+        limit[r] = x_r + lag;
+        shift[r] = x_r == -INFINITY ? 0.f : -x_r * sl2;
+      }
       if (t > 0) {
         // O^T holds the earlier tiles once their products have completed
-        ok &= mbar_wait(bar(L::P_EMPTY + ((n - 1) & 1u)), (n - 1) / 2 & 1u, wctx);
+        ok &= wait_bar(bar(L::P_EMPTY + ((n - 1) & 1u)), (n - 1) / 2 & 1u, wctx);
         tc_fence_after();
         float a[N];
 #pragma unroll
@@ -977,21 +1034,21 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
       }
     }
     // P^T: row r of the buffer holds the weights of query row r, 64 keys to a 128-byte row of a chunk
-    if (n >= 2) ok &= mbar_wait(bar(L::P_EMPTY + (n & 1u)), (n / 2 - 1) & 1u, wctx);
-    uint8_t* pb = gbase + L::OFF_P + (n & 1u) * 2 * L::RCHUNK + (key >> 6) * L::RCHUNK + (key & 7) * 2;
-    const uint32_t unit = (uint32_t)(key & 63) >> 3;
+    if (n >= 2) ok &= wait_bar(bar(L::P_EMPTY + (n & 1u)), (n / 2 - 1) & 1u, wctx);
+    // (16-byte units of a row are swizzled by the row: bits 4 - 6 of the address)
+    const uint32_t pb = base + L::OFF_P + (n & 1u) * 2 * L::RCHUNK + (key >> 6) * L::RCHUNK + (key & 63) * 2;
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-      const float e = ex2_approx(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+      const float e = ex2_approx(fmaf(s[r], sl2, shift[r]));
       l[r] += e;
-      *reinterpret_cast<uint16_t*>(pb + r * 128 + ((unit ^ (r & 7)) << 4)) = round16<BF>(e);
+      st_shared_u16((pb ^ ((r & 7) << 4)) + r * 128, round16<BF>(e));
     }
     if (x.n < 128) {
       // the tile ends behind the last token: rows x.n .. of V are whatever was there before
 #pragma unroll
       for (int h = 0; h < L::PARTS; ++h) {
         const uint32_t i = (2 * n + 1) * L::PARTS + h, st = i % NS;
-        ok &= mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx);
+        ok &= wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx);
         zero_rows(gbase + st * L::SLOT, L::PCH, L::CHUNK, x.n);
       }
     }
@@ -1002,15 +1059,15 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   // ---- the end of the segment: row sums over the threads, then column `key` of each row
   const float total = group_join<N>(l, lane, wq, id, ex + (ex_no++ & 1u) * 32, sum_op);  // of row lane % N
   float factor = 1.0f;
-  if (sg.direct) factor = total > 0.f ? 1.0f / total : 0.f;
+  if (sg.direct) factor = total > 0.f ? __fdividef(1.0f, total) : 0.f;
   if (key < rows) {  // (warp 0)
     if (!(total <= 3.0e38f) && (sg.own || p.lens[key / p.R] >= 0)) atomicCAS(p.err, kDevOk, kDevRange);
     if (!sg.direct)
-      static_cast<float2*>(sg.ml_dst)[key] = make_float2(m_lane, total);
+      static_cast<float2*>(sg.ml_dst)[key] = make_float2(m_lane * sl2, total);
     else if (sg.ml_dst != nullptr)
-      static_cast<float*>(sg.ml_dst)[key] = log_sum(m_lane, total);
+      static_cast<float*>(sg.ml_dst)[key] = log_sum(m_lane * sl2, total);
   }
-  ok &= mbar_wait(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
+  ok &= wait_bar(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
   tc_fence_after();
   uint32_t u[L::PARTS][N];
 #pragma unroll
@@ -1019,23 +1076,22 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   tc_fence_before();
   mbar_arrive(bar(L::O_FREE + (seg_no & 1u)));
   const bool write = D >= 128 || key < D;
-  const int esize = sg.direct ? 2 : 4;
-  uint8_t* dst = sg.o_dst + key * esize;
+  if (sg.direct) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(sg.o_dst) + key;
 #pragma unroll
-  for (int r = 0; r < N; ++r) {
-    const float f = __shfl_sync(0xffffffffu, factor, r);
+    for (int r = 0; r < N; ++r) {
+      const float f = __shfl_sync(0xffffffffu, factor, r);
 #pragma unroll
-    for (int h = 0; h < L::PARTS; ++h) {
-      const float v = __uint_as_float(u[h][r]) * f;
-      uint8_t* at = dst + h * 128 * esize;
-      if (write && r < rows) {
-        if (sg.direct)
-          *reinterpret_cast<uint16_t*>(at) = round16<BF>(v);
-        else
-          *reinterpret_cast<float*>(at) = v;
-      }
+      for (int h = 0; h < L::PARTS; ++h)
+        if (write && r < rows) dst[r * D + h * 128] = round16<BF>(__uint_as_float(u[h][r]) * f);
     }
-    dst += D * esize;
+  } else {
+    float* dst = reinterpret_cast<float*>(sg.o_dst) + key;
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+#pragma unroll
+      for (int h = 0; h < L::PARTS; ++h)
+        if (write && r < rows) dst[r * D + h * 128] = __uint_as_float(u[h][r]);
   }
   return !group_any(id, !ok);
 }
@@ -1044,7 +1100,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
 template <int D, bool BF>
 __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParams& p, SegRing& segs, uint32_t base,
                                          uint32_t bars, uint32_t tmem, volatile uint32_t* asked_for,
-                                         const WaitCtx& wctx) {
+                                         const Waits& wctx) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS, NQ = L::NQ;
   constexpr int PARTS = L::PARTS;
@@ -1068,7 +1124,7 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
       int page = has_box ? look_up(p, sg, x, row0) : 0;
       if (v == 0) {
         const uint32_t qb = seg_no % NQ;
-        if (seg_no >= NQ && !(ok = mbar_wait(bar(L::Q_EMPTY + qb), (seg_no / NQ - 1) & 1u, wctx))) break;
+        if (seg_no >= NQ && !(ok = wait_bar(bar(L::Q_EMPTY + qb), (seg_no / NQ - 1) & 1u, wctx))) break;
         const int rows = sg.rows[0];
         if (lane == 0) mbar_arrive_expect_tx(bar(L::Q_FULL + qb), (uint32_t)rows * 128u * L::KCH);
         __syncwarp();
@@ -1087,7 +1143,7 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) {
           const uint32_t st = (i + h) % NS;
-          if (!(ok = mbar_wait(bar(L::KV_EMPTY + st), ((i + h) / NS & 1u) ^ 1u, wctx))) break;
+          if (!(ok = wait_bar(bar(L::KV_EMPTY + st), ((i + h) / NS & 1u) ^ 1u, wctx))) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(L::KV_FULL + st), bytes);
           __syncwarp();
           if (has_box && row0 < y.n)
@@ -1131,19 +1187,20 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
         cols = sg.rows[0] <= 16 ? 16 : 32;
       }
       const uint32_t qb = seg_no % NQ;
-      if (t == 0 && !(ok = mbar_wait(bar(L::Q_FULL + qb), seg_no / NQ & 1u, wctx))) return f;
+      if (t == 0 && !(ok = wait_bar(bar(L::Q_FULL + qb), seg_no / NQ & 1u, wctx))) return f;
 #pragma unroll
       for (int h = 0; h < PARTS; ++h) {
         const uint32_t i = 2 * n_s * PARTS + h, st = i % NS;
-        if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) return f;
+        if (!(ok = wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx))) return f;
         tc_fence_after();
         const uint64_t dk = sdesc_add(dK0, st * L::SLOT);
         const uint64_t dq = sdesc_add(dQ0, (qb * L::KCH + h * L::PCH) * L::RCHUNK);
+#pragma unroll 1
+        for (int c = 0; c < L::PCH; ++c)
 #pragma unroll
-        for (int k = 0; k < 4 * L::PCH; ++k)
-          mma_ss(tmem + L::T_S(n_s & 3u), sdesc_add(dk, (k / 4) * L::CHUNK + (k % 4) * 32),
-                 sdesc_add(dq, (k / 4) * L::RCHUNK + (k % 4) * 32), idesc_s | (cols >> 3) << 17,
-                 (h > 0 || k > 0) ? 1u : 0u, leader);
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + L::T_S(n_s & 3u), sdesc_add(dk, c * L::CHUNK + k * 32), sdesc_add(dq, c * L::RCHUNK + k * 32),
+                   idesc_s | (cols >> 3) << 17, h + c + k, leader);
         mma_commit(bar(L::KV_EMPTY + st), leader);
       }
       const uint32_t w = seg_no & 1u;
@@ -1163,18 +1220,20 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
     if (ok) f1 = issue_s();
     for (uint32_t n = 0; ok && f0.valid; ++n) {
       const uint32_t par = f0.seg_no & 1u;
-      if (f0.first && f0.seg_no >= 2 && !(ok = mbar_wait(bar(L::O_FREE + par), (f0.seg_no / 2 - 1) & 1u, wctx))) break;
-      if (!(ok = mbar_wait(bar(L::P_FULL + (n & 1u)), n / 2 & 1u, wctx))) break;
+      if (f0.first && f0.seg_no >= 2 && !(ok = wait_bar(bar(L::O_FREE + par), (f0.seg_no / 2 - 1) & 1u, wctx))) break;
+      if (!(ok = wait_bar(bar(L::P_FULL + (n & 1u)), n / 2 & 1u, wctx))) break;
 #pragma unroll
       for (int h = 0; h < PARTS; ++h) {
         const uint32_t i = (2 * n + 1) * PARTS + h, st = i % NS;
-        if (!(ok = mbar_wait(bar(L::KV_FULL + st), i / NS & 1u, wctx))) break;
+        if (!(ok = wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx))) break;
         tc_fence_after();
         const uint64_t dv = sdesc_add(dV0, st * L::SLOT), dp = sdesc_add(dP0, (n & 1u) * 2 * L::RCHUNK);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + L::T_O(par, h), sdesc_add(dv, k * 2048), sdesc_add(dp, (k / 4) * L::RCHUNK + (k % 4) * 32),
-                 idesc_o | (f0.cols >> 3) << 17, (!f0.first || k > 0) ? 1u : 0u, leader);
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + L::T_O(par, h), sdesc_add(dv, (4 * c + k) * 2048), sdesc_add(dp, c * L::RCHUNK + k * 32),
+                   idesc_o | (f0.cols >> 3) << 17, (uint32_t)!f0.first + c + k, leader);
         mma_commit(bar(L::KV_EMPTY + st), leader);
       }
       if (!ok) break;
@@ -1190,17 +1249,18 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
 
 // Warps 4 - 11: softmax, the two warpgroups take segments in turn.
 template <int D, bool BF>
-__device__ __forceinline__ void few_softmax(const PagedParams& p, SegRing& segs, uint8_t* gbase, uint32_t bars,
-                                            uint32_t tmem, const WaitCtx& wctx) {
+__device__ __forceinline__ void few_softmax(const PagedParams& p, SegRing& segs, uint32_t base, uint8_t* gbase, uint32_t bars,
+                                            uint32_t tmem, const Waits& wctx) {
   Seg sg;
   const int w = (int)(threadIdx.x >> 7) - 1;
   uint32_t kv = 0, seg_no = 0, s_no = 0;
   for (; segs.next(sg, wctx); kv += sg.t1 - sg.t0, ++seg_no) {
     if ((seg_no & 1u) != (uint32_t)w) continue;
     const int rows = sg.rows[0];
-    const bool ok = rows <= 8    ? few_segment<D, BF, 8>(p, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
-                    : rows <= 16 ? few_segment<D, BF, 16>(p, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no)
-                                 : few_segment<D, BF, 32>(p, sg, bars, gbase, tmem, wctx, w, kv, seg_no, s_no);
+    const bool ok = rows <= 4    ? few_segment<D, BF, 4>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                    : rows <= 8  ? few_segment<D, BF, 8>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                    : rows <= 16 ? few_segment<D, BF, 16>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                                 : few_segment<D, BF, 32>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no);
     if (!ok) break;
   }
 }
@@ -1217,7 +1277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + M::OFF_BAR;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + M::OFF_ABORT);
-  const WaitCtx wctx{abort_flag, p.err};
+  const Waits wctx{base + M::OFF_ABORT};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Start& start = *reinterpret_cast<Start*>(gbase + M::OFF_START);
 
@@ -1311,6 +1371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (!*abort_flag) return true;
     if (threadIdx.x == 0) {
+      atomicExch(p.err, kDevTimeout);
       if (few)
         drain_ring<Few<D>::NS>(bars + 8u * (M::FEW_BAR + Few<D>::KV_FULL), Few<D>::PARTS, asked_for);
       else
@@ -1342,7 +1403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool do_own = both || (phase == 0) == own_first;
       const bool few = do_own ? p.own_few : p.pre_few;
       if (few)
-        few_softmax<D, BF>(p, segs, gbase, bars + 8u * M::FEW_BAR, tmem, wctx);
+        few_softmax<D, BF>(p, segs, base, gbase, bars + 8u * M::FEW_BAR, tmem, wctx);
       else
         dense_softmax<D, BF>(p, segs, gbase, bars + 8u * M::DENSE_BAR, tmem, wctx);
       if (!phase_end(few)) break;
