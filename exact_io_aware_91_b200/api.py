@@ -519,15 +519,21 @@ def fa_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, causal: bool = False, scale:
 # belongs to the stream they run on.
 
 _PAGED_DTYPES = {torch.bfloat16: FA_BF16, torch.float16: FA_F16}
+_LL3 = ctypes.c_longlong * 3
+# the handle alone where torch offers it: 0.1 us, a Stream object takes 3 us of a call that runs for 10 us
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _launch_on(device: torch.device, stream, fn, *args) -> int:
-    if stream is not None and getattr(stream, "device", device) != device:
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch_on(device, stream, fn, *args)
+    if stream is None:
+        return fn(*args, _current_stream(device.index))
+    if getattr(stream, "device", device) != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream_handle(stream))
-    with torch.cuda.device(device):
-        return fn(*args, _stream_handle(stream))
+    return fn(*args, _stream_handle(stream))
 
 
 def _empty_for(stream, shape, dtype: torch.dtype, device: torch.device) -> torch.Tensor:
@@ -549,12 +555,26 @@ def _cuda_device(t: torch.Tensor) -> torch.device:
     return t.device
 
 
-def _int32(name: str, t: torch.Tensor, device: torch.device, size: int | None = None) -> None:
-    """A dense 1-D int32 array on ``device``."""
+def _int32(name: str, t: torch.Tensor, device: torch.device, size: int | None = None) -> int:
+    """Address of a dense 1-D int32 array on ``device``."""
     if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or not t.is_contiguous() or \
             (size is not None and t.numel() != size):
         what = "" if size is None else f" of {size} elements"
         raise ValueError(f"{name}: expected a contiguous 1-D int32 tensor{what} on {device}")
+    return t.data_ptr()
+
+
+def _dense(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device: torch.device) -> int:
+    """Address of a dense array of that type and shape on ``device``."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _workspace_args(workspace: torch.Tensor, device: torch.device) -> tuple[int, int]:
+    if workspace.device != device:
+        raise ValueError(f"expected the workspace on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _table_dims(block_table: torch.Tensor, device: torch.device) -> tuple[int, int, int]:
@@ -562,50 +582,58 @@ def _table_dims(block_table: torch.Tensor, device: torch.device) -> tuple[int, i
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != device:
         raise ValueError(f"block_table: expected a 2-D int32 tensor on {device}")
     rows, width = block_table.shape
-    step = block_table.stride(0) if rows > 1 else width
-    if (width > 1 and block_table.stride(1) != 1) or step < width:
+    step, one = block_table.stride()
+    if rows <= 1:
+        step = width
+    if (width > 1 and one != 1) or step < width:
         raise ValueError("block_table: the entries of a row must lie side by side and rows must not overlap")
-    return int(rows), int(width), int(step)
+    return rows, width, step
 
 
 def _pool_strides(pool: torch.Tensor) -> tuple[int, int, int]:
     """Elements between pages, heads and tokens of a (num_pages, H_kv, page_size, d) pool."""
     pages, heads, ps, d = pool.shape
-    s = pool.stride()
-    if pool.numel() and d > 1 and s[3] != 1:
+    page, head, token, one = pool.stride()
+    if not pages * heads * ps * d:
+        return heads * ps * d, ps * d, d
+    if d > 1 and one != 1:
         raise ValueError("pages: the d elements of a token must lie side by side")
-    token = s[2] if ps > 1 else d  # the stride of a dimension of one element says nothing
-    head = s[1] if heads > 1 else ps * token
-    page = s[0] if pages > 1 else heads * ps * d
-    return (page, head, token) if pool.numel() else (heads * ps * d, ps * d, d)
+    if ps == 1:  # the stride of a dimension of one element says nothing
+        token = d
+    if heads == 1:
+        head = ps * token
+    if pages == 1:
+        page = heads * ps * d
+    return page, head, token
 
 
 def _paged(q: torch.Tensor, k_pages, v_pages, block_table, H: int, H_kv: int, prefix_len=0, causal=True,
            scale=None) -> FaPagedProblem:
     device = _cuda_device(q)
-    if q.dtype not in _PAGED_DTYPES:
+    dtype = q.dtype
+    if dtype not in _PAGED_DTYPES:
         raise ValueError("expected bf16 or fp16 tensors")
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or int(k_pages.shape[1]) != H_kv or \
-            k_pages.shape[3] != q.shape[3]:
+    B, _, T, d = q.shape
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape or shape[1] != H_kv or shape[3] != d:
         raise ValueError("k_pages and v_pages must be (num_pages, H_kv, page_size, d)")
-    for t in (k_pages, v_pages):
-        if t.dtype != q.dtype or t.device != device:
-            raise ValueError(f"expected pages of {q.dtype} on {device}")
+    if k_pages.dtype != dtype or v_pages.dtype != dtype or k_pages.device != device or v_pages.device != device:
+        raise ValueError(f"expected pages of {dtype} on {device}")
     rows, width, step = _table_dims(block_table, device)
-    B, T, d = int(q.shape[0]), int(q.shape[2]), int(q.shape[3])
     if rows != B:
         raise ValueError(f"block_table has {rows} rows for {B} sequences")
-    ll3 = ctypes.c_longlong * 3
-    return FaPagedProblem(B, H, H_kv, T, d, _PAGED_DTYPES[q.dtype], int(k_pages.shape[2]), int(k_pages.shape[0]), width,
-                          step, int(prefix_len), int(bool(causal)), _scale(scale, d),
-                          ll3(*_pool_strides(k_pages)), ll3(*_pool_strides(v_pages)))
+    return FaPagedProblem(B, H, H_kv, T, d, _PAGED_DTYPES[dtype], shape[2], shape[0], width, step, prefix_len,
+                          1 if causal else 0, d ** -0.5 if scale is None else scale, _LL3(*_pool_strides(k_pages)),
+                          _LL3(*_pool_strides(v_pages)))
 
 
 def paged_problem(q, k_pages, v_pages, block_table, prefix_len: int = 0, causal: bool = True,
                   scale: float | None = None) -> FaPagedProblem:
     """The ``fa_paged_problem`` of these tensors (as ``fa_paged_attn`` takes them)."""
-    H = _shape(q)[1]
-    H_kv = int(k_pages.shape[1]) if k_pages.dim() == 4 else 0
+    if q.dim() != 4:
+        raise ValueError("expected a (B, H, T, d) tensor")
+    H = q.shape[1]
+    H_kv = k_pages.shape[1] if k_pages.dim() == 4 else 0
     if H_kv < 1 or H % H_kv:
         raise ValueError("k_pages must be (num_pages, H_kv, page_size, d), q's head count a multiple of H_kv")
     return _paged(q, k_pages, v_pages, block_table, H, H_kv, prefix_len, causal, scale)
@@ -624,46 +652,44 @@ def fa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, prefix_table=None,
     prefix_table int32 with the pages of ``prefix_len`` tokens that all sequences share.  Returns
     (o, lse).  Rows of negative length are left as they are in ``o`` and ``lse``."""
     pr = paged_problem(q, k_pages, v_pages, block_table, prefix_len, causal, scale)
-    device = q.device
+    device, shape = q.device, q.shape
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
-    _int32("seq_lens", seq_lens, device, pr.B)
-    if pr.prefix_len > 0:
+    lens = _int32("seq_lens", seq_lens, device, shape[0])
+    prefix = None
+    if prefix_len > 0:
         if prefix_table is None:
             raise ValueError("prefix_len needs a prefix_table")
-        _int32("prefix_table", prefix_table, device)
-        if prefix_table.numel() * pr.page_size < pr.prefix_len:
-            raise ValueError(f"prefix_table has {prefix_table.numel()} pages for {pr.prefix_len} tokens")
+        prefix = _int32("prefix_table", prefix_table, device)
+        if prefix_table.numel() * pr.page_size < prefix_len:
+            raise ValueError(f"prefix_table has {prefix_table.numel()} pages for {prefix_len} tokens")
     if o is None:
-        o = _empty_for(stream, q.shape, q.dtype, device)
+        o = _empty_for(stream, shape, q.dtype, device)
     if lse is None:
-        lse = _empty_for(stream, (pr.B, pr.H, pr.T), torch.float32, device)
-    _same(o, dtype=q.dtype, shape=q.shape)
-    _same(lse, dtype=torch.float32, shape=(pr.B, pr.H, pr.T))
+        lse = _empty_for(stream, shape[:3], torch.float32, device)
     if workspace is None:
         workspace = _empty_for(stream, max(fa_paged_attn_workspace_size(pr), 1), torch.uint8, device)
-    if o.device != device or lse.device != device or workspace.device != device:
-        raise ValueError(f"expected o, lse and the workspace on {device}")
     st = _launch_on(device, stream, library().fa_paged_attn, ctypes.byref(pr), q.data_ptr(), k_pages.data_ptr(),
-                    v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-                    prefix_table.data_ptr() if pr.prefix_len > 0 else None, o.data_ptr(), lse.data_ptr(),
-                    workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _check("fa_paged_attn", st)
+                    v_pages.data_ptr(), block_table.data_ptr(), lens, prefix, _dense("o", o, q.dtype, shape, device),
+                    _dense("lse", lse, torch.float32, shape[:3], device), *_workspace_args(workspace, device))
+    if st != FA_OK:
+        raise FAError("fa_paged_attn", st)
     return o, lse
 
 
 def fa_pages_write(k, v, k_pages, v_pages, block_table, seq_lens, stream=None) -> None:
     """Put k, v (B, H_kv, T, d), the T newest tokens of every sequence, into their pages (C
     ``fa_pages_write``): token t of row b goes to position seq_lens[b] - T + t."""
-    B, H_kv, T, d = _shape(k)
+    if k.dim() != 4:
+        raise ValueError("expected (B, H_kv, T, d) tensors")
+    H_kv = k.shape[1]
     pr = _paged(k, k_pages, v_pages, block_table, H_kv, H_kv)
-    _same(k, v, dtype=k.dtype, shape=(B, H_kv, T, d))
-    if v.device != k.device:
-        raise ValueError(f"expected v on {k.device}")
-    _int32("seq_lens", seq_lens, k.device, B)
-    st = _launch_on(k.device, stream, library().fa_pages_write, ctypes.byref(pr), k.data_ptr(), v.data_ptr(),
-                    k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr())
-    _check("fa_pages_write", st)
+    device = k.device
+    st = _launch_on(device, stream, library().fa_pages_write, ctypes.byref(pr), _dense("k", k, k.dtype, k.shape, device),
+                    _dense("v", v, k.dtype, k.shape, device), k_pages.data_ptr(), v_pages.data_ptr(),
+                    block_table.data_ptr(), _int32("seq_lens", seq_lens, device, k.shape[0]))
+    if st != FA_OK:
+        raise FAError("fa_pages_write", st)
 
 
 def fa_pages_workspace_size(rows: int, num_pages: int) -> int:
@@ -673,53 +699,51 @@ def fa_pages_workspace_size(rows: int, num_pages: int) -> int:
 def _planes(planes) -> tuple[FaPagePlanes, torch.device]:
     """``fa_page_planes`` of one (n_planes, num_pages, ...) tensor or of a sequence of
     (num_pages, ...) tensors of one shape, type and layout; each page is dense."""
-    stacked = isinstance(planes, torch.Tensor)
-    if stacked and planes.dim() < 3:
-        raise ValueError("planes: expected a (n_planes, num_pages, ...) tensor")
-    tensors = [planes[0]] if stacked and planes.shape[0] else [] if stacked else list(planes)
-    if not tensors:
-        raise ValueError("planes: expected at least one plane")
-    x = tensors[0]
-    device = _cuda_device(x)
-    if x.dim() < 2:
-        raise ValueError("planes: expected (num_pages, ...) tensors")
-    size = 1
-    for n, step in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        if n > 1 and step != size:
-            raise ValueError("planes: the elements of a page must lie side by side")
-        size *= n
-    for t in tensors:
-        if t.shape != x.shape or t.dtype != x.dtype or t.stride() != x.stride() or t.device != device:
-            raise ValueError("planes: expected tensors of one shape, type, layout and device")
-    pages = int(x.shape[0])
-    esize = x.element_size()
-    if stacked:
-        apart = planes.stride(0) * esize
-        ptrs = [x.data_ptr() + i * apart for i in range(planes.shape[0])]
+    if isinstance(planes, torch.Tensor):
+        x, shape, strides = planes, planes.shape[1:], planes.stride()[1:]
+        if planes.dim() < 3 or not planes.shape[0]:
+            raise ValueError("planes: expected a (n_planes, num_pages, ...) tensor")
+        esize = x.element_size()
+        apart, first = planes.stride(0) * esize, planes.data_ptr()
+        ptrs = [first + i * apart for i in range(planes.shape[0])]
     else:
+        tensors = list(planes)
+        if not tensors:
+            raise ValueError("planes: expected at least one plane")
+        x = tensors[0]
+        _cuda_device(x)
+        shape, strides, dtype, where = x.shape, x.stride(), x.dtype, x.device
+        if len(shape) < 2:
+            raise ValueError("planes: expected (num_pages, ...) tensors")
+        for t in tensors:
+            if t.shape != shape or t.dtype != dtype or t.stride() != strides or t.device != where:
+                raise ValueError("planes: expected tensors of one shape, type, layout and device")
+        esize = x.element_size()
         ptrs = [t.data_ptr() for t in tensors]
-    array = (ctypes.c_void_p * len(ptrs))(*ptrs)
-    step = x.stride(0) if pages > 1 else size
+    size = 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] > 1 and strides[i] != size:
+            raise ValueError("planes: the elements of a page must lie side by side")
+        size *= shape[i]
+    pages = shape[0]
+    step = strides[0] if pages > 1 else size
     if step < size:
         raise ValueError("planes: pages must not overlap")
+    array = (ctypes.c_void_p * len(ptrs))(*ptrs)
     return FaPagePlanes(ctypes.cast(array, ctypes.POINTER(ctypes.c_void_p)), len(ptrs), pages, size * esize,
-                        step * esize), device
+                        step * esize), _cuda_device(x)
 
 
 def _page_table(page_size: int, block_table, seq_lens, ref_counts) -> tuple[FaPageTable, torch.device]:
     device = _cuda_device(block_table)
     rows, width, step = _table_dims(block_table, device)
-    _int32("seq_lens", seq_lens, device, rows)
-    _int32("ref_counts", ref_counts, device)
-    return FaPageTable(rows, width, step, int(page_size), ref_counts.numel(), block_table.data_ptr(),
-                       seq_lens.data_ptr(), ref_counts.data_ptr()), device
+    return FaPageTable(rows, width, step, page_size, ref_counts.numel(), block_table.data_ptr(),
+                       _int32("seq_lens", seq_lens, device, rows), _int32("ref_counts", ref_counts, device)), device
 
 
 def _pages_workspace(workspace, table: FaPageTable, device: torch.device, stream) -> torch.Tensor:
     if workspace is None:
         return _empty_for(stream, fa_pages_workspace_size(table.rows, table.num_pages), torch.uint8, device)
-    if workspace.device != device:
-        raise ValueError(f"expected the workspace on {device}")
     return workspace
 
 
@@ -727,10 +751,9 @@ def fa_pages_copy(planes, src, dst, stream=None) -> None:
     """Page dst[i] = page src[i] in every plane (C ``fa_pages_copy``).  planes: one (n_planes,
     num_pages, ...) tensor, or a sequence of (num_pages, ...) tensors (K and V of every layer)."""
     pl, device = _planes(planes)
-    _int32("src", src, device)
-    _int32("dst", dst, device, src.numel())
-    st = _launch_on(device, stream, library().fa_pages_copy, ctypes.byref(pl), src.data_ptr(), dst.data_ptr(),
-                    src.numel())
+    n = src.numel()
+    st = _launch_on(device, stream, library().fa_pages_copy, ctypes.byref(pl), _int32("src", src, device),
+                    _int32("dst", dst, device, n), n)
     _check("fa_pages_copy", st)
 
 
@@ -738,10 +761,10 @@ def fa_pages_reserve(page_size: int, block_table, seq_lens, ref_counts, new_lens
     """Pages for new_lens[b] tokens of every row b (C ``fa_pages_reserve``); updates block_table,
     seq_lens and ref_counts."""
     table, device = _page_table(page_size, block_table, seq_lens, ref_counts)
-    _int32("new_lens", new_lens, device, table.rows)
+    lens = _int32("new_lens", new_lens, device, table.rows)
     ws = _pages_workspace(workspace, table, device, stream)
-    st = _launch_on(device, stream, library().fa_pages_reserve, ctypes.byref(table), new_lens.data_ptr(), ws.data_ptr(),
-                    ws.numel() * ws.element_size())
+    st = _launch_on(device, stream, library().fa_pages_reserve, ctypes.byref(table), lens,
+                    *_workspace_args(ws, device))
     _check("fa_pages_reserve", st)
 
 
@@ -753,19 +776,19 @@ def fa_pages_fork(planes, page_size: int, block_table, seq_lens, ref_counts, par
     table, table_device = _page_table(page_size, block_table, seq_lens, ref_counts)
     if table_device != device:
         raise ValueError(f"expected the table on {device}")
-    _int32("parents", parents, device)
-    _int32("children", children, device, parents.numel())
+    n = parents.numel()
     ws = _pages_workspace(workspace, table, device, stream)
-    st = _launch_on(device, stream, library().fa_pages_fork, ctypes.byref(pl), ctypes.byref(table), parents.data_ptr(),
-                    children.data_ptr(), parents.numel(), ws.data_ptr(), ws.numel() * ws.element_size())
+    st = _launch_on(device, stream, library().fa_pages_fork, ctypes.byref(pl), ctypes.byref(table),
+                    _int32("parents", parents, device), _int32("children", children, device, n), n,
+                    *_workspace_args(ws, device))
     _check("fa_pages_fork", st)
 
 
 def fa_pages_free(page_size: int, block_table, seq_lens, ref_counts, rows, stream=None) -> None:
     """Take back the pages of the given rows (C ``fa_pages_free``)."""
     table, device = _page_table(page_size, block_table, seq_lens, ref_counts)
-    _int32("rows", rows, device)
-    st = _launch_on(device, stream, library().fa_pages_free, ctypes.byref(table), rows.data_ptr(), rows.numel())
+    st = _launch_on(device, stream, library().fa_pages_free, ctypes.byref(table), _int32("rows", rows, device),
+                    rows.numel())
     _check("fa_pages_free", st)
 
 
@@ -778,22 +801,20 @@ def fa_pages_compact(planes, page_size: int, block_table, seq_lens, ref_counts, 
     table, table_device = _page_table(page_size, block_table, seq_lens, ref_counts)
     if table_device != device:
         raise ValueError(f"expected the table on {device}")
+    rows, width, step, pages = table.rows, table.max_pages, table.table_stride, table.num_pages
     if block_table_out is None:
-        block_table_out = _empty_for(stream, (table.rows, table.table_stride), torch.int32,
-                                     device)[:, :table.max_pages]
+        block_table_out = _empty_for(stream, (rows, step), torch.int32, device)[:, :width]
     if ref_counts_out is None:
-        ref_counts_out = _empty_for(stream, table.num_pages, torch.int32, device)
+        ref_counts_out = _empty_for(stream, pages, torch.int32, device)
     if page_map is None:
-        page_map = _empty_for(stream, table.num_pages, torch.int32, device)
-    if _table_dims(block_table_out, device)[:2] != (table.rows, table.max_pages) or \
-            (table.rows > 1 and block_table_out.stride(0) != table.table_stride):
+        page_map = _empty_for(stream, pages, torch.int32, device)
+    out_rows, out_width, out_step = _table_dims(block_table_out, device)
+    if (out_rows, out_width) != (rows, width) or (rows > 1 and out_step != step):
         raise ValueError("block_table_out: expected the shape and row stride of block_table")
-    _int32("ref_counts_out", ref_counts_out, device, table.num_pages)
-    _int32("page_map", page_map, device, table.num_pages)
     ws = _pages_workspace(workspace, table, device, stream)
     st = _launch_on(device, stream, library().fa_pages_compact, ctypes.byref(pl), ctypes.byref(table),
-                    block_table_out.data_ptr(), ref_counts_out.data_ptr(), page_map.data_ptr(), ws.data_ptr(),
-                    ws.numel() * ws.element_size())
+                    block_table_out.data_ptr(), _int32("ref_counts_out", ref_counts_out, device, pages),
+                    _int32("page_map", page_map, device, pages), *_workspace_args(ws, device))
     _check("fa_pages_compact", st)
     return block_table_out, ref_counts_out, page_map
 

@@ -46,6 +46,7 @@
 // less than 8 in base 2); sums, maxima and O are fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <atomic>
 
 #include "paged.h"
 #include "sm100.cuh"
@@ -1281,6 +1282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Start& start = *reinterpret_cast<Start*>(gbase + M::OFF_START);
 
+  // The joining kernel may be set up as soon as multiprocessors get free; it waits for this one's end.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < M::NBAR) {
     // arrivals: the 128 threads of a warpgroup where P, O or statistics are handed over, the reading
     // warps of a segment, else 1
@@ -1425,6 +1428,7 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   const int r = (int)(row - bk * p.R), b = (int)(bk / p.H_kv), hk = (int)(bk - (long long)b * p.H_kv);
   const int len = own_len(p, b);
   if (len < 0) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   const int rc = r / ITEM;
   const int nt = own_tiles(p, len, own_visible<ITEM>(p, len, rc));
   const bool pre = p.packed && p.prefix_len > 0;
@@ -1480,16 +1484,25 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
 #pragma unroll
     for (int i = 0; i < E; ++i) o[i] *= a;
     const int m32 = min(32, n - i0);
-    for (int k = 0; k < m32; ++k) {
-      const float ck = __shfl_sync(0xffffffffu, c, k);
-      const long long wk = __shfl_sync(0xffffffffu, where, k);
-      const float* src = (i0 + k < n_own ? p.own_o : p.pre_o) + wk * D + lane * E;
+    for (int k0 = 0; k0 < m32; k0 += 4) {  // four parts' loads in flight
+      float2 v[4][E / 2];
+      float ck[4];
 #pragma unroll
-      for (int i = 0; i < E; i += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + i);
-        o[i] = fmaf(ck, v.x, o[i]);
-        o[i + 1] = fmaf(ck, v.y, o[i + 1]);
+      for (int k = 0; k < 4; ++k) {
+        ck[k] = __shfl_sync(0xffffffffu, c, k0 + k);
+        const long long wk = __shfl_sync(0xffffffffu, where, k0 + k);
+        const float* src = (i0 + k0 + k < n_own ? p.own_o : p.pre_o) + wk * D + lane * E;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+          v[k][i] = k0 + k < m32 ? *reinterpret_cast<const float2*>(src + 2 * i) : make_float2(0.f, 0.f);
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          o[2 * i] = fmaf(ck[k], v[k][i].x, o[2 * i]);
+          o[2 * i + 1] = fmaf(ck[k], v[k][i].y, o[2 * i + 1]);
+        }
     }
   }
   const float inv = L > 0.f ? 1.0f / L : 0.f;
@@ -1504,13 +1517,28 @@ template <int D, bool BF>
 cudaError_t launch(const PagedMaps& maps, const PagedParams& p, cudaStream_t s) {
   constexpr int smem = Smem<D>::ALLOC;
   auto kernel = fa_paged_attn_sm100_kernel<D, BF>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<bool> ready[64];  // per device: the kernel's shared memory size is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
   kernel<<<p.ctas, kThreads, smem, s>>>(maps, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = (long long)p.B * p.H * p.T;
-  fa_paged_join_kernel<D, BF><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_paged_join_kernel<D, BF>, p);
 }
 
 template <bool BF>
