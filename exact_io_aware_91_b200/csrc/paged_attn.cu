@@ -19,9 +19,12 @@
 // and so are those of the prefix items; a CTA walks its part of both lines.  So ragged lengths load
 // all multiprocessors equally, without the host knowing them: every CTA adds up the lengths itself.
 // A part that covers an item only partly leaves (m, l, O) in the workspace, and a second kernel joins
-// the parts of each row in the order of the line (the same on every run).  CTAs with an odd
-// number walk the own line first: own items wait for memory (each key is used for R rows only),
-// prefix items for the tensor core, and the two overlap across the device.
+// the parts of each row in the order of the line (the same on every run).  Half of the CTAs walk the
+// own line first: own items wait for memory (each key is used for R rows only), prefix items for the
+// tensor core, and the two overlap across the device.  The halves are whole pairs of neighbouring
+// multiprocessors (by smid): two neighbours in different code slow each other down by fetching
+// instructions (128 sequences over a prefix of 32785 tokens: 150 us with neighbours in different lines,
+// 113 us so, 117 us with the prefix first everywhere).
 //
 // Two forms of a tile's products:
 //   dense  S = Q K^T and O += P V with the query rows as the 128 rows of the product, for items of
@@ -1363,7 +1366,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Both lines in one phase where they take the same form, else one phase each.
   const bool pre = p.packed && p.prefix_len > 0, both = !pre || p.pre_few == p.own_few;
-  const bool own_first = (blockIdx.x & 1) != 0;
+  uint32_t smid;
+  asm volatile("mov.u32 %0, %%smid;" : "=r"(smid));
+  const bool own_first = (smid >> 1 & 1u) != 0;
   const int phases = both ? 1 : 2;
   volatile uint32_t* asked_for = reinterpret_cast<volatile uint32_t*>(gbase + M::OFF_ISSUED);
   // False if a wait gave up: the CTA ends then.
