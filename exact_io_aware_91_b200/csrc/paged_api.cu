@@ -163,8 +163,10 @@ fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k
   p.n_groups = w.n_groups;
   p.own_few = w.own_few;
   p.pre_few = w.pre_few;
-  p.own_kt = w.own_few || d != 256 ? 7 : 6;  // 128 keys; two 128-row tiles at d = 256 leave room for 64
-  p.pre_kt = w.pre_few || d != 256 ? 7 : 6;
+  // keys per tile: 128; 64 in the dense form at d = 256 (tensor memory), 256 in the few-rows form at d = 64
+  const int few_kt = d == 64 ? 8 : 7, dense_kt = d == 256 ? 6 : 7;
+  p.own_kt = w.own_few ? few_kt : dense_kt;
+  p.pre_kt = w.pre_few ? few_kt : dense_kt;
   p.pre_tiles = (pr->prefix_len + (1 << p.pre_kt) - 1) >> p.pre_kt;
   p.ctas = std::min(num_sms, kPagedMaxCtas);
   p.scale_log2 = pr->scale * 1.4426950408889634f;

@@ -87,28 +87,34 @@ struct Dense {
   static_assert(2 * KT <= 256 && 256 + NWG * D <= 512, "tensor memory columns");
 };
 
-// The same of the few-rows form.  A ring slot holds 128 keys x up to 128 columns.
+// The same of the few-rows form.  A ring slot holds 128 keys x up to 128 columns; a tile is 128 keys,
+// at d = 64 256 keys (two per softmax thread: what a step costs apart from its keys, waits and
+// barriers of some 1000 cycles, then falls on 64 KB of keys and values, as at d = 128).
 template <int D>
 struct Few {
+  static constexpr int KPT = D == 64 ? 2 : 1;        // keys per thread
+  static constexpr int KT = 128 * KPT;
   static constexpr int KCH = D / 64;
-  static constexpr int PARTS = D == 256 ? 2 : 1;     // slots per K or V tile
-  static constexpr int PCH = KCH / PARTS;            // chunks per slot
+  static constexpr int PARTS_D = D == 256 ? 2 : 1;   // slots per K or V tile along the columns
+  static constexpr int PARTS = PARTS_D * KPT;        // slots per K or V tile
+  static constexpr int PCH = KCH / PARTS_D;          // chunks per slot
   static constexpr int CHUNK = 128 * 128;
   static constexpr int SLOT = PCH * CHUNK;
-  static constexpr int NS = D == 64 ? 11 : 5;
+  static constexpr int NS = D == 64 ? 10 : 5;
   static constexpr int NQ = D == 256 ? 2 : 4;        // query buffers
   static constexpr int RCHUNK = kFewRows * 128;      // one chunk (64 columns or keys) of Q or P^T
+  static constexpr int PBUF = 2 * KPT * RCHUNK;      // 32 rows x the tile's keys
   static constexpr int OFF_Q = NS * SLOT;
-  static constexpr int OFF_P = OFF_Q + NQ * KCH * RCHUNK;  // [2] buffers of 32 rows x 128 keys
-  static constexpr int OFF_EX = OFF_P + 2 * 2 * RCHUNK;    // float[2 warpgroups][2][32][4]
+  static constexpr int OFF_P = OFF_Q + NQ * KCH * RCHUNK;  // [2]
+  static constexpr int OFF_EX = OFF_P + 2 * PBUF;          // float[2 warpgroups][2][32][4]
   static constexpr int END = OFF_EX + 2048;
   // the product of d = 64 takes 128 columns of V: the second 64 are whatever follows the slot
   static_assert(D != 64 || OFF_Q + CHUNK <= END, "the last slot's neighbour is inside shared memory");
   static constexpr int Q_FULL = 0, Q_EMPTY = NQ, S_FULL = 2 * NQ, P_FULL = S_FULL + 4, P_EMPTY = P_FULL + 2;
   static constexpr int O_FULL = P_EMPTY + 2, O_FREE = O_FULL + 2, MMA_DONE = O_FREE + 2, KV_FULL = MMA_DONE + 1;
   static constexpr int KV_EMPTY = KV_FULL + NS, NBAR = KV_EMPTY + NS;
-  static __host__ __device__ constexpr uint32_t T_S(int i) { return i * kFewRows; }                          // [4]
-  static __host__ __device__ constexpr uint32_t T_O(int i, int h) { return 128 + (i * 2 + h) * kFewRows; }   // [2][2]
+  static __host__ __device__ constexpr uint32_t T_S(int i, int h) { return (i * 2 + h) * kFewRows; }        // [4][2]
+  static __host__ __device__ constexpr uint32_t T_O(int i, int h) { return 256 + (i * 2 + h) * kFewRows; }  // [2][2]
 };
 
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
@@ -943,6 +949,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
                                             uint32_t seg_no, uint32_t& s_no) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS;
+  constexpr int KPT = L::KPT;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
   const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, key = wq * 32 + lane;
   const uint32_t lanes = (uint32_t)(wq * 32) << 16;
@@ -973,38 +980,51 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
 #pragma unroll 1
   for (int t = 0; t < n_tiles; ++t, ++s_no) {
     const uint32_t n = kv + t;  // step of the phase
-    const TileInfo x = tile_info<128>(p, sg, sg.t0 + t);
+    const TileInfo x = tile_info<L::KT>(p, sg, sg.t0 + t);
     ok &= wait_bar(bar(L::S_FULL + 2 * w + (s_no & 1u)), s_no / 2 & 1u, wctx);
     tc_fence_after();
-    float s[N];
+    float s[KPT][N];  // of keys `key` (and key + 128)
     {
-      uint32_t u[N];
-      tmem_ld<N>(tmem + lanes + L::T_S(n & 3u), u);
+      uint32_t u[KPT][N];
+#pragma unroll
+      for (int g = 0; g < KPT; ++g) tmem_ld<N>(tmem + lanes + L::T_S(n & 3u, g), u[g]);
       tmem_wait_ld();
 #pragma unroll
-      for (int r = 0; r < N; ++r) s[r] = __uint_as_float(u[r]);
+      for (int g = 0; g < KPT; ++g)
+#pragma unroll
+        for (int r = 0; r < N; ++r) s[g][r] = __uint_as_float(u[g][r]);
     }
     // keys that a row does not see; all rows see the same ones, except own keys with several causal tokens
     if (!x.pre && p.causal && p.T > 1) {
       const int lim0 = sg.len - p.T + 1 - x.k0;  // of the first token
-      if (lim0 < 128) {
+      if (lim0 < L::KT) {
         int tok = 0;
 #pragma unroll
         for (int r = 0; r < N; ++r) {
-          if (key >= lim0 + tok) s[r] = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < KPT; ++g)
+            if (key + 128 * g >= lim0 + tok) s[g][r] = -INFINITY;
           if (++tok == p.T) tok = 0;
         }
       }
-    } else if (key >= x.n) {
+    } else {
 #pragma unroll
-      for (int r = 0; r < N; ++r) s[r] = -INFINITY;
+      for (int g = 0; g < KPT; ++g)
+        if (key + 128 * g >= x.n) {
+#pragma unroll
+          for (int r = 0; r < N; ++r) s[g][r] = -INFINITY;
+        }
     }
+    float top[N];  // the larger one of the thread's keys
     bool above = false;
 #pragma unroll
-    for (int r = 0; r < N; ++r) above |= s[r] > limit[r];
+    for (int r = 0; r < N; ++r) {
+      top[r] = KPT == 2 ? fmaxf(s[0][r], s[KPT - 1][r]) : s[0][r];
+      above |= top[r] > limit[r];
+    }
     if (group_any(id, above)) {
       // a maximum has moved by 2^8 or more (always on the first tile): take the tile's maxima
-      const float t_max = group_join<N>(s, lane, wq, id, ex + (ex_no++ & 1u) * 32, fmax_op);
+      const float t_max = group_join<N>(top, lane, wq, id, ex + (ex_no++ & 1u) * 32, fmax_op);
       const float m_new = fmaxf(m_lane, t_max);
       const float m_use = m_new > m_lane + lag ? m_new : m_lane;
       const float alpha = m_use == m_lane ? 1.0f : ex2_approx((m_lane - m_use) * sl2);
@@ -1026,7 +1046,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
           l[r] *= a[r];
         }
 #pragma unroll
-        for (int h = 0; h < L::PARTS; ++h) {
+        for (int h = 0; h < L::PARTS_D; ++h) {
           uint32_t u[N];
           tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u);
           tmem_wait_ld();
@@ -1040,20 +1060,22 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
     // P^T: row r of the buffer holds the weights of query row r, 64 keys to a 128-byte row of a chunk
     if (n >= 2) ok &= wait_bar(bar(L::P_EMPTY + (n & 1u)), (n / 2 - 1) & 1u, wctx);
     // (16-byte units of a row are swizzled by the row: bits 4 - 6 of the address)
-    const uint32_t pb = base + L::OFF_P + (n & 1u) * 2 * L::RCHUNK + (key >> 6) * L::RCHUNK + (key & 63) * 2;
+    const uint32_t pb = base + L::OFF_P + (n & 1u) * L::PBUF + (key >> 6) * L::RCHUNK + (key & 63) * 2;
 #pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float e = ex2_approx(fmaf(s[r], sl2, shift[r]));
-      l[r] += e;
-      st_shared_u16((pb ^ ((r & 7) << 4)) + r * 128, round16<BF>(e));
-    }
-    if (x.n < 128) {
+    for (int g = 0; g < KPT; ++g)
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float e = ex2_approx(fmaf(s[g][r], sl2, shift[r]));
+        l[r] += e;
+        st_shared_u16((pb ^ ((r & 7) << 4)) + r * 128 + g * 2 * L::RCHUNK, round16<BF>(e));
+      }
+    if (x.n < L::KT) {
       // the tile ends behind the last token: rows x.n .. of V are whatever was there before
 #pragma unroll
       for (int h = 0; h < L::PARTS; ++h) {
         const uint32_t i = (2 * n + 1) * L::PARTS + h, st = i % NS;
         ok &= wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx);
-        zero_rows(gbase + st * L::SLOT, L::PCH, L::CHUNK, x.n);
+        zero_rows(gbase + st * L::SLOT, L::PCH, L::CHUNK, KPT == 2 ? min(128, max(0, x.n - 128 * h)) : x.n);
       }
     }
     fence_proxy_async_smem();
@@ -1073,9 +1095,9 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   }
   ok &= wait_bar(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
   tc_fence_after();
-  uint32_t u[L::PARTS][N];
+  uint32_t u[L::PARTS_D][N];
 #pragma unroll
-  for (int h = 0; h < L::PARTS; ++h) tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u[h]);
+  for (int h = 0; h < L::PARTS_D; ++h) tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u[h]);
   tmem_wait_ld();
   tc_fence_before();
   mbar_arrive(bar(L::O_FREE + (seg_no & 1u)));
@@ -1086,7 +1108,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
     for (int r = 0; r < N; ++r) {
       const float f = __shfl_sync(0xffffffffu, factor, r);
 #pragma unroll
-      for (int h = 0; h < L::PARTS; ++h)
+      for (int h = 0; h < L::PARTS_D; ++h)
         if (write && r < rows) dst[r * D + h * 128] = round16<BF>(__uint_as_float(u[h][r]) * f);
     }
   } else {
@@ -1094,7 +1116,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
 #pragma unroll
     for (int r = 0; r < N; ++r)
 #pragma unroll
-      for (int h = 0; h < L::PARTS; ++h)
+      for (int h = 0; h < L::PARTS_D; ++h)
         if (write && r < rows) dst[r * D + h * 128] = __uint_as_float(u[h][r]);
   }
   return !group_any(id, !ok);
@@ -1116,7 +1138,7 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
     // ===================================================== page lookup and TMA: Q and K, or V
     const int v = warp >> 1;
     const CUtensorMap* map = v ? &maps.v : &maps.k;
-    const int per_chunk = 128 / p.box_rows;
+    const int per_chunk = L::KT / p.box_rows;  // at most 32 boxes per slot or, at d = 64, pair of slots
     const int chunk = lane / per_chunk, row0 = (lane - chunk * per_chunk) * p.box_rows;
     const bool has_box = chunk < L::PCH;
     const int page_mask = (1 << p.page_shift) - 1;
@@ -1124,7 +1146,7 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
     uint32_t issued = 0;                 // ring index behind the last slot asked for
     bool ok = true;
     for (; ok && segs.next(sg, wctx); ++seg_no) {
-      TileInfo x = tile_info<128>(p, sg, sg.t0);
+      TileInfo x = tile_info<L::KT>(p, sg, sg.t0);
       int page = has_box ? look_up(p, sg, x, row0) : 0;
       if (v == 0) {
         const uint32_t qb = seg_no % NQ;
@@ -1140,18 +1162,22 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
         const TileInfo y = x;
         const int cur = page;
         if (t + 1 < sg.t1) {
-          x = tile_info<128>(p, sg, t + 1);
+          x = tile_info<L::KT>(p, sg, t + 1);
           if (has_box) page = look_up(p, sg, x, row0);
         }
-        const uint32_t bytes = (uint32_t)((y.n + p.box_rows - 1) / p.box_rows) * p.box_rows * 128u * L::PCH;
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) {
           const uint32_t st = (i + h) % NS;
           if (!(ok = wait_bar(bar(L::KV_EMPTY + st), ((i + h) / NS & 1u) ^ 1u, wctx))) break;
-          if (lane == 0) mbar_arrive_expect_tx(bar(L::KV_FULL + st), bytes);
+          // slot h: columns from 128 h on (d = 256), or keys from 128 h on (d = 64)
+          const int first = L::KPT == 2 ? 128 * h : 0, col = L::KPT == 2 ? 0 : h * L::PCH;
+          const int rows = min(128, max(0, y.n - first));
+          if (lane == 0)
+            mbar_arrive_expect_tx(bar(L::KV_FULL + st),
+                                  (uint32_t)((rows + p.box_rows - 1) / p.box_rows) * p.box_rows * 128u * L::PCH);
           __syncwarp();
-          if (has_box && row0 < y.n)
-            tma_load_4d(base + st * L::SLOT + chunk * L::CHUNK + row0 * 128, map, (h * L::PCH + chunk) * 64,
+          if (has_box && row0 >= first && row0 < first + rows)
+            tma_load_4d(base + st * L::SLOT + chunk * L::CHUNK + (row0 - first) * 128, map, (col + chunk) * 64,
                         (y.k0 + row0) & page_mask, sg.hk, cur, bar(L::KV_FULL + st));
           issued = i + h + 1;
         }
@@ -1198,13 +1224,14 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
         if (!(ok = wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx))) return f;
         tc_fence_after();
         const uint64_t dk = sdesc_add(dK0, st * L::SLOT);
-        const uint64_t dq = sdesc_add(dQ0, (qb * L::KCH + h * L::PCH) * L::RCHUNK);
+        const uint64_t dq = sdesc_add(dQ0, (qb * L::KCH + (L::KPT == 2 ? 0 : h * L::PCH)) * L::RCHUNK);
+        const uint32_t d_s = tmem + L::T_S(n_s & 3u, L::KPT == 2 ? h : 0);
 #pragma unroll 1
         for (int c = 0; c < L::PCH; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ss(tmem + L::T_S(n_s & 3u), sdesc_add(dk, c * L::CHUNK + k * 32), sdesc_add(dq, c * L::RCHUNK + k * 32),
-                   idesc_s | (cols >> 3) << 17, h + c + k, leader);
+            mma_ss(d_s, sdesc_add(dk, c * L::CHUNK + k * 32), sdesc_add(dq, c * L::RCHUNK + k * 32),
+                   idesc_s | (cols >> 3) << 17, (L::KPT == 2 ? 0 : h) + c + k, leader);
         mma_commit(bar(L::KV_EMPTY + st), leader);
       }
       const uint32_t w = seg_no & 1u;
@@ -1231,13 +1258,15 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
         const uint32_t i = (2 * n + 1) * PARTS + h, st = i % NS;
         if (!(ok = wait_bar(bar(L::KV_FULL + st), i / NS & 1u, wctx))) break;
         tc_fence_after();
-        const uint64_t dv = sdesc_add(dV0, st * L::SLOT), dp = sdesc_add(dP0, (n & 1u) * 2 * L::RCHUNK);
+        const uint64_t dv = sdesc_add(dV0, st * L::SLOT);
+        const uint64_t dp = sdesc_add(dP0, (n & 1u) * L::PBUF + (L::KPT == 2 ? 2 * h * L::RCHUNK : 0));
+        const uint32_t d_o = tmem + L::T_O(par, L::KPT == 2 ? 0 : h);
 #pragma unroll 1
         for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ss(tmem + L::T_O(par, h), sdesc_add(dv, (4 * c + k) * 2048), sdesc_add(dp, c * L::RCHUNK + k * 32),
-                   idesc_o | (f0.cols >> 3) << 17, (uint32_t)!f0.first + c + k, leader);
+            mma_ss(d_o, sdesc_add(dv, (4 * c + k) * 2048), sdesc_add(dp, c * L::RCHUNK + k * 32),
+                   idesc_o | (f0.cols >> 3) << 17, (uint32_t)!f0.first + (L::KPT == 2 ? h : 0) + c + k, leader);
         mma_commit(bar(L::KV_EMPTY + st), leader);
       }
       if (!ok) break;
