@@ -45,6 +45,13 @@ fa_status check_paged(const fa_paged_problem* p, bool queries, bool* empty) {
       (long long)p->B * p->table_stride > (1ll << 40))
     return FA_ERR_UNSUPPORTED;
   *empty = p->B == 0 || p->T == 0;
+  if (queries && !*empty) {
+    // all (item, key tile) units, with one more per item, are counted in 32 bits
+    const PagedWs w = paged_ws_layout(p->B, p->H, p->H_kv, p->T, p->d);
+    const long long own = ((long long)p->max_pages * p->page_size + 63) / 64, pre = (p->prefix_len + 63ll) / 64;
+    if (w.own_items > 0x7fffffffLL / (own + pre + 1) || w.pre_items > 0x7fffffffLL / (pre + 1))
+      return FA_ERR_UNSUPPORTED;
+  }
   return FA_OK;
 }
 

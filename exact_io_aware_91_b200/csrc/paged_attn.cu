@@ -319,27 +319,33 @@ __device__ __forceinline__ int own_tiles(const PagedParams& p, int len, int visi
 __device__ __forceinline__ int item_units(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
 
 template <int ITEM>
-__device__ long long units_of(const PagedParams& p, int b) {
+__device__ int units_of(const PagedParams& p, int b) {
   const int len = own_len(p, b);
-  long long n = 0;
+  int n = 0;
   for (int rc = 0; rc < p.n_rc; ++rc) n += item_units(own_tiles(p, len, own_visible<ITEM>(p, len, rc)));
   return n * p.H_kv;
 }
 
-// A line of n units is cut into line_parts(n) parts, none of them empty: part c has the units from
-// part_begin(c) on, and unit u is in part part_of(u).  The own line's parts go to the CTAs in falling
+// A line of n units (fewer than 2^31, which the host sees to) in `parts` parts, none of them empty: the
+// first `more` have size + 1 units, the others `size`.  The own line's parts go to the CTAs in falling
 // order, so that a short prefix line and a short own line fall to different CTAs.
-__device__ __forceinline__ int line_parts(const PagedParams& p, long long n) {
-  return n < p.ctas ? (int)n : p.ctas;
-}
-__device__ __forceinline__ long long part_begin(long long n, int parts, int c) { return n * c / parts; }
-__device__ __forceinline__ int part_of(long long n, int parts, long long u) {
-  return (int)(((u + 1) * parts - 1) / n);
-}
+struct Line {
+  int parts, size, more;
+  __device__ __forceinline__ Line(int n, int ctas) {
+    parts = min(n, ctas);
+    size = parts > 0 ? (int)((unsigned)n / (unsigned)parts) : 0;
+    more = n - size * parts;
+  }
+  __device__ __forceinline__ int begin(int part) const { return part * size + min(part, more); }
+  __device__ __forceinline__ int part_of(int u) const {  // the part that holds unit u
+    const int lead = more * (size + 1);
+    return u < lead ? (int)((unsigned)u / (unsigned)(size + 1)) : more + (int)((unsigned)(u - lead) / (unsigned)size);
+  }
+};
 
 struct Start {  // where a CTA's part of the own line begins
-  long long total;  // units of the whole line
-  long long left;   // units of this CTA
+  int total;          // units of the whole line
+  int left;           // units of this CTA
   int b, rc, hk, at;  // item, and the unit inside it
 };
 
@@ -349,15 +355,15 @@ struct Walk {
   static constexpr int NWG = Dense<D>::NWG, ITEM = 128 * NWG;
   const PagedParams& p;
   const Start& start;
-  long long pre_u, pre_end, own_left;
+  int pre_u, pre_end, own_left;
   int b, rc, hk, at;
   int cur_b, len;
 
   __device__ Walk(const PagedParams& p_, const Start& s, bool pre, bool own) : p(p_), start(s) {
-    const long long n = pre ? (long long)p.n_groups * p.H_kv * p.pre_tiles : 0;
-    const int parts = line_parts(p, n), c = blockIdx.x;
-    pre_u = c < parts ? part_begin(n, parts, c) : 0;
-    pre_end = c < parts ? part_begin(n, parts, c + 1) : 0;
+    const Line line(pre ? p.n_groups * p.H_kv * p.pre_tiles : 0, p.ctas);
+    const int c = blockIdx.x;
+    pre_u = c < line.parts ? line.begin(c) : 0;
+    pre_end = c < line.parts ? line.begin(c + 1) : 0;
     own_left = own ? s.left : 0;
     b = s.b;
     rc = s.rc;
@@ -367,13 +373,13 @@ struct Walk {
     len = 0;
   }
   // Where the results go.
-  __device__ void place(Seg& s, bool whole, long long item, long long items, int part, int item_rows, long long out_row) {
+  __device__ void place(Seg& s, bool whole, int item, int items, int part, int item_rows, long long out_row) {
     s.direct = whole && s.own && (!p.packed || p.prefix_len == 0);
     if (s.direct) {
       s.o_dst = static_cast<uint8_t*>(p.o) + out_row * (2 * D);
       s.ml_dst = p.lse != nullptr ? p.lse + out_row : nullptr;
     } else {
-      const long long row = (whole ? item : items + 2 * part + (s.t0 == 0 ? 1 : 0)) * item_rows;
+      const long long row = (long long)(whole ? item : items + 2 * part + (s.t0 == 0 ? 1 : 0)) * item_rows;
       s.o_dst = reinterpret_cast<uint8_t*>((s.own ? p.own_o : p.pre_o) + row * D);
       s.ml_dst = (s.own ? p.own_ml : p.pre_ml) + row;
     }
@@ -381,19 +387,19 @@ struct Walk {
   __device__ bool next(Seg& s, bool own_first) {
     if (own_first && next_own(s)) return true;
     if (pre_u < pre_end) {
-      const long long item = pre_u / p.pre_tiles;
+      const int item = (int)((unsigned)pre_u / (unsigned)p.pre_tiles);
       s.own = 0;
-      s.hk = (int)(item / p.n_groups);
-      s.b = (int)(item - (long long)s.hk * p.n_groups) * p.seqs * NWG;
+      s.hk = (int)((unsigned)item / (unsigned)p.n_groups);
+      s.b = (item - s.hk * p.n_groups) * p.seqs * NWG;
       s.row0 = s.len = s.visible = 0;
       s.lead = p.pre_tiles;
-      s.t0 = (int)(pre_u - item * p.pre_tiles);
-      s.t1 = (int)min((long long)p.pre_tiles, s.t0 + (pre_end - pre_u));
+      s.t0 = pre_u - item * p.pre_tiles;
+      s.t1 = min(p.pre_tiles, s.t0 + (pre_end - pre_u));
       s.pair = NWG == 2 && s.b + p.seqs < p.B;
       s.rows[0] = min(p.seqs, p.B - s.b) * p.R;
       s.rows[1] = s.pair ? min(p.seqs, p.B - s.b - p.seqs) * p.R : 0;
       pre_u += s.t1 - s.t0;
-      place(s, s.t0 == 0 && s.t1 == p.pre_tiles, item, (long long)p.n_groups * p.H_kv, blockIdx.x, ITEM, 0);
+      place(s, s.t0 == 0 && s.t1 == p.pre_tiles, item, p.n_groups * p.H_kv, blockIdx.x, ITEM, 0);
       return true;
     }
     return next_own(s);
@@ -408,7 +414,7 @@ struct Walk {
       const int nt = own_tiles(p, len, vis);
       int t0 = 0, t1 = 0;
       if (nt > 0) {
-        const int end = (int)min((long long)(nt + kItemCost), at + own_left);
+        const int end = min(nt + kItemCost, at + own_left);
         t0 = max(0, at - kItemCost);
         t1 = max(0, end - kItemCost);
         own_left -= end - at;
@@ -438,14 +444,14 @@ struct Walk {
         s.t0 = t0;
         s.t1 = t1;
         const int part = p.ctas - 1 - (int)blockIdx.x;
-        const long long item = ((long long)s.b * p.n_rc + rc0) * p.H_kv + s.hk;
-        place(s, t0 == 0 && t1 == nt, item, p.packed ? (long long)p.B * p.n_rc * p.H_kv : 0, part, min(p.R, ITEM),
+        const int item = (s.b * p.n_rc + rc0) * p.H_kv + s.hk;
+        place(s, t0 == 0 && t1 == nt, item, p.packed ? p.B * p.n_rc * p.H_kv : 0, part, min(p.R, ITEM),
               ((long long)s.b * p.H_kv + s.hk) * p.R + s.row0);
         if (t0 == 0 && threadIdx.x % 32 == 0) {  // for the joining kernel: which parts of the line hold the item
           int last = part;
           if (t1 < nt) {  // its last unit is nt - t1 units behind this part
-            const int parts = line_parts(p, start.total);
-            last = part_of(start.total, parts, part_begin(start.total, parts, part + 1) + (nt - t1) - 1);
+            const Line line(start.total, p.ctas);
+            last = line.part_of(line.begin(part + 1) + (nt - t1) - 1);
           }
           p.seg[item] = make_int2(part, last);
         }
@@ -1340,48 +1346,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- this CTA's part of the own line: every thread adds up the units of its share of the
   // sequences, the block scans the sums, and the thread whose share holds the part's first unit finds it
   {
-    long long* scan = reinterpret_cast<long long*>(gbase + M::OFF_SCAN);
+    int* scan = reinterpret_cast<int*>(gbase + M::OFF_SCAN);
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-    long long mine = 0;
+    int mine = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       mine += units_of<ITEM>(p, b);
       if (blockIdx.x == 0 && p.lens[b] > ((long long)p.max_pages << p.page_shift))
         atomicExch(p.err, kDevIndex);  // a length that the table cannot hold
     }
-    long long x = mine;
+    int x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, d);
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
       if (lane >= d) x += y;
     }
     if (lane == 31) scan[warp] = x;
     __syncthreads();
-    long long before = 0, total = 0;
+    int before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) before += scan[w];
       total += scan[w];
     }
     before += x - mine;
-    const int parts = line_parts(p, total), part = p.ctas - 1 - (int)blockIdx.x;
-    const long long lo = part < parts ? part_begin(total, parts, part) : 0;
-    const long long hi = part < parts ? part_begin(total, parts, part + 1) : 0;
+    const Line line(total, p.ctas);
+    const int part = p.ctas - 1 - (int)blockIdx.x;
+    const int lo = part < line.parts ? line.begin(part) : 0, hi = part < line.parts ? line.begin(part + 1) : 0;
     if (hi > lo && before <= lo && lo < before + mine) {
-      long long skip = lo - before;
+      int skip = lo - before;
       int b = b0;
-      for (long long n; b < b1 && skip >= (n = units_of<ITEM>(p, b)); ++b) skip -= n;
+#pragma unroll 1
+      for (int n; b < b1 && skip >= (n = units_of<ITEM>(p, b)); ++b) skip -= n;
       const int len = own_len(p, b);
+#pragma unroll 1
       for (int rc = 0; rc < p.n_rc; ++rc) {
         const int n = item_units(own_tiles(p, len, own_visible<ITEM>(p, len, rc)));
-        if (skip >= (long long)n * p.H_kv) {
-          skip -= (long long)n * p.H_kv;
+        if (skip >= n * p.H_kv) {
+          skip -= n * p.H_kv;
           continue;
         }
         start.b = b;
         start.rc = rc;
-        start.hk = (int)(skip / n);
-        start.at = (int)(skip - (long long)start.hk * n);
+        start.hk = (int)((unsigned)skip / (unsigned)n);
+        start.at = skip - start.hk * n;
         start.left = hi - lo;
         break;
       }
@@ -1466,25 +1475,23 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   const int rc = r / ITEM;
   const int nt = own_tiles(p, len, own_visible<ITEM>(p, len, rc));
   const bool pre = p.packed && p.prefix_len > 0;
-  const long long item = ((long long)b * p.n_rc + rc) * p.H_kv + hk;
+  const int item = (b * p.n_rc + rc) * p.H_kv + hk;
   int2 own = make_int2(0, -1), pc = make_int2(0, -1);
   if (nt > 0) {
     own = p.seg[item];
     if (own.x == own.y && !pre) return;  // written at once
   }
-  long long pre_item = 0, pre_row = 0;
+  int pre_item = 0, pre_row = 0;
   if (pre) {
     const int per = p.seqs * NWG, g = b / per, in = b - g * per;
-    pre_item = (long long)hk * p.n_groups + g;
+    pre_item = hk * p.n_groups + g;
     pre_row = (in / p.seqs) * 128 + (in % p.seqs) * p.R + r;
-    const long long n = (long long)p.n_groups * p.H_kv * p.pre_tiles, u = pre_item * p.pre_tiles;
-    const int parts = line_parts(p, n);
-    pc.x = part_of(n, parts, u);
-    pc.y = part_of(n, parts, u + p.pre_tiles - 1);
+    const Line line(p.n_groups * p.H_kv * p.pre_tiles, p.ctas);
+    pc.x = line.part_of(pre_item * p.pre_tiles);
+    pc.y = line.part_of(pre_item * p.pre_tiles + p.pre_tiles - 1);
   }
   const int n_own = own.y - own.x + 1, n = n_own + pc.y - pc.x + 1;
-  const long long own_items = p.packed ? (long long)p.B * p.n_rc * p.H_kv : 0;
-  const long long pre_items = (long long)p.n_groups * p.H_kv;
+  const int own_items = p.packed ? p.B * p.n_rc * p.H_kv : 0, pre_items = p.n_groups * p.H_kv;
   // where part i's row lies, counted in rows of its array
   auto at = [&](int i) -> long long {
     const bool o = i < n_own;

@@ -49,6 +49,7 @@ BAD_ATTN = [
     (dict(H=7), "INVALID_ARG"), (dict(H=0), "INVALID_ARG"), (dict(prefix_len=-1), "INVALID_ARG"),
     (dict(causal=2), "INVALID_ARG"), (dict(scale=0.0), "INVALID_ARG"), (dict(scale=float("nan")), "INVALID_ARG"),
     (dict(scale=float("inf")), "INVALID_ARG"), (dict(prefix_len=(1 << 30) + 1), "UNSUPPORTED"),
+    (dict(B=1 << 20, max_pages=1 << 16, table_stride=1 << 16), "UNSUPPORTED"),  # 2^31 units and more
 ]
 
 
