@@ -323,8 +323,8 @@ fa_status fa_pages_compact(const fa_page_planes* planes, const fa_page_table* ta
   if (st != FA_OK) return st;
   if ((st = check_planes(planes)) != FA_OK) return st;
   if (planes->num_pages != t.num_pages) return FA_ERR_INVALID_ARG;
-  if (t.num_pages == 0) return FA_OK;
-  if (!ref_counts_out || !page_map || (t.rows > 0 && t.max_pages > 0 && !block_table_out)) return FA_ERR_INVALID_ARG;
+  if ((t.num_pages > 0 && (!ref_counts_out || !page_map)) || (t.rows > 0 && t.max_pages > 0 && !block_table_out))
+    return FA_ERR_INVALID_ARG;
   if ((st = check_table_ptrs(t)) != FA_OK) return st;
   if (!aligned(block_table_out, 4) || !aligned(ref_counts_out, 4) || !aligned(page_map, 4)) return FA_ERR_MISALIGNED;
   if ((st = check_ws(workspace, workspace_bytes, fa_pages_workspace_size(t.rows, t.num_pages))) != FA_OK) return st;

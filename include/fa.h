@@ -368,8 +368,9 @@ typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
  * fa_paged_attn -- attention of the newest T tokens of every sequence over its pages, with a
  * prefix that the whole batch shares (a system prompt, a document): the prefix's keys and
  * values are read once for all sequences instead of once per sequence.
- *   q, o            : (B, H, T, d) of `dtype`, 16-byte aligned, contiguous; lse: fp32 (B, H, T)
- *                     or NULL.  T >= 1: 1 for decoding, more for drafts or a prompt's chunk.
+ *   q, o            : (B, H, T, d) of `dtype`, 16-byte aligned, contiguous, o apart from every
+ *                     input; lse: fp32 (B, H, T) or NULL.  T is 1 for decoding, more for drafts
+ *                     or a prompt's chunk.
  *   block_table, seq_lens : of the B sequences; seq_lens[b] counts the sequence's own tokens,
  *                     the T new ones included (their K, V are in the pages already) and the
  *                     shared prefix not.
@@ -381,7 +382,8 @@ typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
  * Query head h reads key/value head h / (H / H_kv).  A query that sees no key gets o = 0 and
  * lse = -inf.  Rows with seq_lens[b] < 0 are left as they were in o and lse.  Whatever lies in
  * pages behind a sequence's last token (or behind prefix_len), infinities and NaN included, does
- * not reach the outputs.
+ * not reach the outputs.  A visible key, value or query that is not finite, or a score beyond the
+ * fp32 range, makes its rows unspecified (FA_ERR_RANGE from fa_last_device_status).
  * Products run in `dtype` with fp32 accumulation, the softmax in fp32; the probabilities are
  * rounded to `dtype` for the P V product (the row sum takes the rounded values), and o once at
  * the end.  d is 64, 128 or 256.  The result does not depend on timing: partial sums are joined
@@ -389,6 +391,8 @@ typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
  *   workspace       : fa_paged_attn_workspace_size(problem) bytes, 256-byte aligned; contents on
  *                     entry do not matter; one call at a time per workspace.  The size depends
  *                     on B, H, H_kv, T and d only, not on lengths.
+ * FA_ERR_UNSUPPORTED also when items (sequences x key/value heads x 256 rows) times key tiles of the
+ * longest sequence that the table holds reach 2^31.
  */
 typedef struct fa_paged_problem {
   int B, H, H_kv, T, d;
