@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -129,7 +130,7 @@ def library() -> ctypes.CDLL:
     lib.fa_attn_fwd_fp8.restype = i
     lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f, i, vp]
     lib.fa_bwd_noalloc.restype = i
-    pg, pt, pl = (ctypes.POINTER(t) for t in (FaPagedProblem, FaPageTable, FaPagePlanes))
+    pg = pt = pl = vp  # fa_paged_problem, fa_page_table, fa_page_planes: a byref() or packed bytes
     lib.fa_paged_attn_workspace_size.argtypes = [pg]
     lib.fa_paged_attn_workspace_size.restype = sz
     lib.fa_paged_attn.argtypes = [pg, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
@@ -519,14 +520,23 @@ def fa_bwd_noalloc(q, k, v, o, do, lse, dq, dk, dv, causal: bool = False, scale:
 # belongs to the stream they run on.
 
 _PAGED_DTYPES = {torch.bfloat16: FA_BF16, torch.float16: FA_F16}
-_LL3 = ctypes.c_longlong * 3
+# fa_paged_problem, fa_page_table and fa_page_planes as bytes: a quarter of the time of filling in a
+# ctypes structure, in calls that take the GPU a few microseconds
+_PROBLEM = struct.Struct("@12if6q")
+_TABLE = struct.Struct("@5i3P")
+_PLANES = struct.Struct("@P2i2q")
+assert (_PROBLEM.size, _TABLE.size, _PLANES.size) == tuple(
+    ctypes.sizeof(t) for t in (FaPagedProblem, FaPageTable, FaPagePlanes))
 # the handle alone where torch offers it: 0.1 us, a Stream object takes 3 us of a call that runs for 10 us
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _launch_on(device: torch.device, stream, fn, *args) -> int:
-    if device.index != torch.cuda.current_device():
+    if device.index != _current_device():
         with torch.cuda.device(device):
             return _launch_on(device, stream, fn, *args)
     if stream is None:
@@ -590,9 +600,9 @@ def _table_dims(block_table: torch.Tensor, device: torch.device) -> tuple[int, i
     return rows, width, step
 
 
-def _pool_strides(pool: torch.Tensor) -> tuple[int, int, int]:
+def _pool_strides(pool: torch.Tensor, shape) -> tuple[int, int, int]:
     """Elements between pages, heads and tokens of a (num_pages, H_kv, page_size, d) pool."""
-    pages, heads, ps, d = pool.shape
+    pages, heads, ps, d = shape
     page, head, token, one = pool.stride()
     if not pages * heads * ps * d:
         return heads * ps * d, ps * d, d
@@ -607,36 +617,45 @@ def _pool_strides(pool: torch.Tensor) -> tuple[int, int, int]:
     return page, head, token
 
 
-def _paged(q: torch.Tensor, k_pages, v_pages, block_table, H: int, H_kv: int, prefix_len=0, causal=True,
-           scale=None) -> FaPagedProblem:
-    device = _cuda_device(q)
+def _paged(q: torch.Tensor, k_pages, v_pages, block_table, shape, H: int, H_kv: int, prefix_len, causal, scale,
+           device: torch.device) -> bytes:
+    """``fa_paged_problem`` of these tensors; ``shape`` is q's."""
     dtype = q.dtype
     if dtype not in _PAGED_DTYPES:
         raise ValueError("expected bf16 or fp16 tensors")
-    B, _, T, d = q.shape
-    shape = k_pages.shape
-    if len(shape) != 4 or v_pages.shape != shape or shape[1] != H_kv or shape[3] != d:
+    B, _, T, d = shape
+    pool = k_pages.shape
+    if len(pool) != 4 or v_pages.shape != pool or pool[1] != H_kv or pool[3] != d:
         raise ValueError("k_pages and v_pages must be (num_pages, H_kv, page_size, d)")
     if k_pages.dtype != dtype or v_pages.dtype != dtype or k_pages.device != device or v_pages.device != device:
         raise ValueError(f"expected pages of {dtype} on {device}")
     rows, width, step = _table_dims(block_table, device)
     if rows != B:
         raise ValueError(f"block_table has {rows} rows for {B} sequences")
-    return FaPagedProblem(B, H, H_kv, T, d, _PAGED_DTYPES[dtype], shape[2], shape[0], width, step, prefix_len,
-                          1 if causal else 0, d ** -0.5 if scale is None else scale, _LL3(*_pool_strides(k_pages)),
-                          _LL3(*_pool_strides(v_pages)))
+    k_stride = _pool_strides(k_pages, pool)
+    v_stride = _pool_strides(v_pages, pool)
+    try:
+        return _PROBLEM.pack(B, H, H_kv, T, d, _PAGED_DTYPES[dtype], pool[2], pool[0], width, step, prefix_len,
+                             1 if causal else 0, d ** -0.5 if scale is None else scale, *k_stride, *v_stride)
+    except struct.error as e:
+        raise ValueError(f"sizes beyond 32 bits, or no numbers: {e}") from None
+
+
+def _attn_problem(q, k_pages, v_pages, block_table, shape, prefix_len, causal, scale, device) -> bytes:
+    if len(shape) != 4:
+        raise ValueError("expected a (B, H, T, d) tensor")
+    H = shape[1]
+    H_kv = k_pages.shape[1] if k_pages.dim() == 4 else 0
+    if H_kv < 1 or H % H_kv:
+        raise ValueError("k_pages must be (num_pages, H_kv, page_size, d), q's head count a multiple of H_kv")
+    return _paged(q, k_pages, v_pages, block_table, shape, H, H_kv, prefix_len, causal, scale, device)
 
 
 def paged_problem(q, k_pages, v_pages, block_table, prefix_len: int = 0, causal: bool = True,
                   scale: float | None = None) -> FaPagedProblem:
     """The ``fa_paged_problem`` of these tensors (as ``fa_paged_attn`` takes them)."""
-    if q.dim() != 4:
-        raise ValueError("expected a (B, H, T, d) tensor")
-    H = q.shape[1]
-    H_kv = k_pages.shape[1] if k_pages.dim() == 4 else 0
-    if H_kv < 1 or H % H_kv:
-        raise ValueError("k_pages must be (num_pages, H_kv, page_size, d), q's head count a multiple of H_kv")
-    return _paged(q, k_pages, v_pages, block_table, H, H_kv, prefix_len, causal, scale)
+    return FaPagedProblem.from_buffer_copy(
+        _attn_problem(q, k_pages, v_pages, block_table, q.shape, prefix_len, causal, scale, _cuda_device(q)))
 
 
 def fa_paged_attn_workspace_size(problem: FaPagedProblem) -> int:
@@ -651,8 +670,8 @@ def fa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, prefix_table=None,
     that keep a token's d elements together; block_table (B, max_pages) and seq_lens (B) int32;
     prefix_table int32 with the pages of ``prefix_len`` tokens that all sequences share.  Returns
     (o, lse).  Rows of negative length are left as they are in ``o`` and ``lse``."""
-    pr = paged_problem(q, k_pages, v_pages, block_table, prefix_len, causal, scale)
-    device, shape = q.device, q.shape
+    device, shape = _cuda_device(q), q.shape
+    pr = _attn_problem(q, k_pages, v_pages, block_table, shape, prefix_len, causal, scale, device)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     lens = _int32("seq_lens", seq_lens, device, shape[0])
@@ -661,15 +680,15 @@ def fa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, prefix_table=None,
         if prefix_table is None:
             raise ValueError("prefix_len needs a prefix_table")
         prefix = _int32("prefix_table", prefix_table, device)
-        if prefix_table.numel() * pr.page_size < prefix_len:
+        if prefix_table.numel() * k_pages.shape[2] < prefix_len:
             raise ValueError(f"prefix_table has {prefix_table.numel()} pages for {prefix_len} tokens")
     if o is None:
         o = _empty_for(stream, shape, q.dtype, device)
     if lse is None:
         lse = _empty_for(stream, shape[:3], torch.float32, device)
     if workspace is None:
-        workspace = _empty_for(stream, max(fa_paged_attn_workspace_size(pr), 1), torch.uint8, device)
-    st = _launch_on(device, stream, library().fa_paged_attn, ctypes.byref(pr), q.data_ptr(), k_pages.data_ptr(),
+        workspace = _empty_for(stream, max(library().fa_paged_attn_workspace_size(pr), 1), torch.uint8, device)
+    st = _launch_on(device, stream, library().fa_paged_attn, pr, q.data_ptr(), k_pages.data_ptr(),
                     v_pages.data_ptr(), block_table.data_ptr(), lens, prefix, _dense("o", o, q.dtype, shape, device),
                     _dense("lse", lse, torch.float32, shape[:3], device), *_workspace_args(workspace, device))
     if st != FA_OK:
@@ -680,14 +699,13 @@ def fa_paged_attn(q, k_pages, v_pages, block_table, seq_lens, prefix_table=None,
 def fa_pages_write(k, v, k_pages, v_pages, block_table, seq_lens, stream=None) -> None:
     """Put k, v (B, H_kv, T, d), the T newest tokens of every sequence, into their pages (C
     ``fa_pages_write``): token t of row b goes to position seq_lens[b] - T + t."""
-    if k.dim() != 4:
+    device, shape = _cuda_device(k), k.shape
+    if len(shape) != 4:
         raise ValueError("expected (B, H_kv, T, d) tensors")
-    H_kv = k.shape[1]
-    pr = _paged(k, k_pages, v_pages, block_table, H_kv, H_kv)
-    device = k.device
-    st = _launch_on(device, stream, library().fa_pages_write, ctypes.byref(pr), _dense("k", k, k.dtype, k.shape, device),
-                    _dense("v", v, k.dtype, k.shape, device), k_pages.data_ptr(), v_pages.data_ptr(),
-                    block_table.data_ptr(), _int32("seq_lens", seq_lens, device, k.shape[0]))
+    pr = _paged(k, k_pages, v_pages, block_table, shape, shape[1], shape[1], 0, True, 1.0, device)
+    st = _launch_on(device, stream, library().fa_pages_write, pr, _dense("k", k, k.dtype, shape, device),
+                    _dense("v", v, k.dtype, shape, device), k_pages.data_ptr(), v_pages.data_ptr(),
+                    block_table.data_ptr(), _int32("seq_lens", seq_lens, device, shape[0]))
     if st != FA_OK:
         raise FAError("fa_pages_write", st)
 
@@ -696,8 +714,8 @@ def fa_pages_workspace_size(rows: int, num_pages: int) -> int:
     return int(library().fa_pages_workspace_size(rows, num_pages))
 
 
-def _planes(planes) -> tuple[FaPagePlanes, torch.device]:
-    """``fa_page_planes`` of one (n_planes, num_pages, ...) tensor or of a sequence of
+def _planes(planes) -> tuple[bytes, object, torch.device]:
+    """``fa_page_planes`` (and the array of addresses that it points to) of one (n_planes, num_pages, ...) tensor or of a sequence of
     (num_pages, ...) tensors of one shape, type and layout; each page is dense."""
     if isinstance(planes, torch.Tensor):
         x, shape, strides = planes, planes.shape[1:], planes.stride()[1:]
@@ -729,30 +747,31 @@ def _planes(planes) -> tuple[FaPagePlanes, torch.device]:
     step = strides[0] if pages > 1 else size
     if step < size:
         raise ValueError("planes: pages must not overlap")
+    device = _cuda_device(x)
     array = (ctypes.c_void_p * len(ptrs))(*ptrs)
-    return FaPagePlanes(ctypes.cast(array, ctypes.POINTER(ctypes.c_void_p)), len(ptrs), pages, size * esize,
-                        step * esize), _cuda_device(x)
+    return _PLANES.pack(ctypes.addressof(array), len(ptrs), pages, size * esize, step * esize), array, device
 
 
-def _page_table(page_size: int, block_table, seq_lens, ref_counts) -> tuple[FaPageTable, torch.device]:
+def _page_table(page_size: int, block_table, seq_lens, ref_counts) -> tuple[bytes, torch.device]:
     device = _cuda_device(block_table)
     rows, width, step = _table_dims(block_table, device)
-    return FaPageTable(rows, width, step, page_size, ref_counts.numel(), block_table.data_ptr(),
-                       _int32("seq_lens", seq_lens, device, rows), _int32("ref_counts", ref_counts, device)), device
+    return _TABLE.pack(rows, width, step, page_size, ref_counts.numel(), block_table.data_ptr(),
+                       _int32("seq_lens", seq_lens, device, rows),
+                       _int32("ref_counts", ref_counts, device)), device
 
 
-def _pages_workspace(workspace, table: FaPageTable, device: torch.device, stream) -> torch.Tensor:
+def _pages_workspace(workspace, seq_lens, ref_counts, device: torch.device, stream) -> torch.Tensor:
     if workspace is None:
-        return _empty_for(stream, fa_pages_workspace_size(table.rows, table.num_pages), torch.uint8, device)
+        return _empty_for(stream, fa_pages_workspace_size(seq_lens.numel(), ref_counts.numel()), torch.uint8, device)
     return workspace
 
 
 def fa_pages_copy(planes, src, dst, stream=None) -> None:
     """Page dst[i] = page src[i] in every plane (C ``fa_pages_copy``).  planes: one (n_planes,
     num_pages, ...) tensor, or a sequence of (num_pages, ...) tensors (K and V of every layer)."""
-    pl, device = _planes(planes)
+    pl, array, device = _planes(planes)  # (the array lives until the call is over)
     n = src.numel()
-    st = _launch_on(device, stream, library().fa_pages_copy, ctypes.byref(pl), _int32("src", src, device),
+    st = _launch_on(device, stream, library().fa_pages_copy, pl, _int32("src", src, device),
                     _int32("dst", dst, device, n), n)
     _check("fa_pages_copy", st)
 
@@ -761,9 +780,9 @@ def fa_pages_reserve(page_size: int, block_table, seq_lens, ref_counts, new_lens
     """Pages for new_lens[b] tokens of every row b (C ``fa_pages_reserve``); updates block_table,
     seq_lens and ref_counts."""
     table, device = _page_table(page_size, block_table, seq_lens, ref_counts)
-    lens = _int32("new_lens", new_lens, device, table.rows)
-    ws = _pages_workspace(workspace, table, device, stream)
-    st = _launch_on(device, stream, library().fa_pages_reserve, ctypes.byref(table), lens,
+    lens = _int32("new_lens", new_lens, device, seq_lens.numel())
+    ws = _pages_workspace(workspace, seq_lens, ref_counts, device, stream)
+    st = _launch_on(device, stream, library().fa_pages_reserve, table, lens,
                     *_workspace_args(ws, device))
     _check("fa_pages_reserve", st)
 
@@ -772,13 +791,13 @@ def fa_pages_fork(planes, page_size: int, block_table, seq_lens, ref_counts, par
                   stream=None) -> None:
     """Row children[i] continues from row parents[i] (C ``fa_pages_fork``): full pages are shared,
     a partly filled last page is copied in every plane (planes as for ``fa_pages_copy``)."""
-    pl, device = _planes(planes)
+    pl, array, device = _planes(planes)
     table, table_device = _page_table(page_size, block_table, seq_lens, ref_counts)
     if table_device != device:
         raise ValueError(f"expected the table on {device}")
     n = parents.numel()
-    ws = _pages_workspace(workspace, table, device, stream)
-    st = _launch_on(device, stream, library().fa_pages_fork, ctypes.byref(pl), ctypes.byref(table),
+    ws = _pages_workspace(workspace, seq_lens, ref_counts, device, stream)
+    st = _launch_on(device, stream, library().fa_pages_fork, pl, table,
                     _int32("parents", parents, device), _int32("children", children, device, n), n,
                     *_workspace_args(ws, device))
     _check("fa_pages_fork", st)
@@ -787,7 +806,7 @@ def fa_pages_fork(planes, page_size: int, block_table, seq_lens, ref_counts, par
 def fa_pages_free(page_size: int, block_table, seq_lens, ref_counts, rows, stream=None) -> None:
     """Take back the pages of the given rows (C ``fa_pages_free``)."""
     table, device = _page_table(page_size, block_table, seq_lens, ref_counts)
-    st = _launch_on(device, stream, library().fa_pages_free, ctypes.byref(table), _int32("rows", rows, device),
+    st = _launch_on(device, stream, library().fa_pages_free, table, _int32("rows", rows, device),
                     rows.numel())
     _check("fa_pages_free", st)
 
@@ -797,11 +816,12 @@ def fa_pages_compact(planes, page_size: int, block_table, seq_lens, ref_counts, 
     """Move the live pages to the front of the pool (C ``fa_pages_compact``; planes as for
     ``fa_pages_copy``).  Returns (block_table_out, ref_counts_out, page_map); the first two may be
     block_table and ref_counts themselves."""
-    pl, device = _planes(planes)
+    pl, array, device = _planes(planes)
     table, table_device = _page_table(page_size, block_table, seq_lens, ref_counts)
     if table_device != device:
         raise ValueError(f"expected the table on {device}")
-    rows, width, step, pages = table.rows, table.max_pages, table.table_stride, table.num_pages
+    rows, width, step = _table_dims(block_table, device)
+    pages = ref_counts.numel()
     if block_table_out is None:
         block_table_out = _empty_for(stream, (rows, step), torch.int32, device)[:, :width]
     if ref_counts_out is None:
@@ -811,8 +831,8 @@ def fa_pages_compact(planes, page_size: int, block_table, seq_lens, ref_counts, 
     out_rows, out_width, out_step = _table_dims(block_table_out, device)
     if (out_rows, out_width) != (rows, width) or (rows > 1 and out_step != step):
         raise ValueError("block_table_out: expected the shape and row stride of block_table")
-    ws = _pages_workspace(workspace, table, device, stream)
-    st = _launch_on(device, stream, library().fa_pages_compact, ctypes.byref(pl), ctypes.byref(table),
+    ws = _pages_workspace(workspace, seq_lens, ref_counts, device, stream)
+    st = _launch_on(device, stream, library().fa_pages_compact, pl, table,
                     block_table_out.data_ptr(), _int32("ref_counts_out", ref_counts_out, device, pages),
                     _int32("page_map", page_map, device, pages), *_workspace_args(ws, device))
     _check("fa_pages_compact", st)
