@@ -88,7 +88,9 @@ struct PagedParams {
   int box_rows;    // tokens per TMA box of K and V
   int packed;      // 1: the prefix has work items of its own, each for the rows of several sequences
   int own_few, pre_few;  // own / prefix items have at most kFewRows rows
-  int seqs;        // packed: sequences per 128-row tile of a prefix item
+  int seqs;        // packed: sequences per query tile of a prefix item
+  int group_seqs;  // packed: sequences per prefix item
+  int pre_rows;    // packed: rows of a prefix item's slot
   int n_rc;        // row chunks of a (sequence, key/value head)
   int n_groups;    // packed: prefix items per key/value head
   int own_kt, pre_kt;  // log2 of the keys per tile
@@ -112,8 +114,11 @@ struct PagedParams {
 struct PagedWs {
   int item_rows;  // rows of an item: 256 (two 128-row tiles), d = 256: 128
   int slot_rows;  // rows of an own slot
-  int packed, own_few, pre_few, seqs, n_rc, n_groups;
-  long long own_items, own_slots, pre_items, pre_slots;
+  int packed, own_few, n_rc;
+  // prefix items in the dense form [0] and in the few-rows form [1]: sequences per query tile and per
+  // item, items per key/value head, rows of a slot
+  int seqs[2], group_seqs[2], n_groups[2], pre_rows[2];
+  long long own_items, own_slots, pre_slots[2];
   size_t off_seg, off_own_ml, off_own_o, off_pre_ml, off_pre_o, total;
 };
 inline PagedWs paged_ws_layout(int B, int H, int H_kv, int T, int d) {
@@ -123,23 +128,40 @@ inline PagedWs paged_ws_layout(int B, int H, int H_kv, int T, int d) {
   w.item_rows = d == 256 ? 128 : 256;
   w.packed = R <= 128;
   w.own_few = R <= kFewRows;
-  w.pre_few = R * B <= kFewRows;  // the rows of the whole batch
-  w.seqs = w.pre_few ? B : w.packed ? (int)(128 / R) : 1;
   w.n_rc = (int)((R + w.item_rows - 1) / w.item_rows);
   w.slot_rows = (int)(R < w.item_rows ? R : w.item_rows);
-  const int per_group = w.seqs * (w.item_rows / 128);  // sequences per prefix item
-  w.n_groups = !w.packed ? 0 : w.pre_few ? 1 : (B + per_group - 1) / per_group;
   w.own_items = (long long)B * w.n_rc * H_kv;
   w.own_slots = (w.packed ? w.own_items : 0) + 2 * kPagedMaxCtas;
-  w.pre_items = (long long)w.n_groups * H_kv;
-  w.pre_slots = w.packed ? w.pre_items + 2 * kPagedMaxCtas : 0;
+  size_t pre_slot_rows = 0;
+  for (int f = 0; f < 2; ++f) {
+    if (!(f ? w.own_few : w.packed)) continue;
+    w.seqs[f] = (int)((f ? kFewRows : 128) / R);
+    if (w.seqs[f] > B) w.seqs[f] = B;
+    w.group_seqs[f] = f ? w.seqs[f] : w.seqs[f] * (w.item_rows / 128);
+    w.n_groups[f] = (B + w.group_seqs[f] - 1) / w.group_seqs[f];
+    w.pre_rows[f] = f ? kFewRows : w.item_rows;
+    w.pre_slots[f] = (long long)w.n_groups[f] * H_kv + 2 * kPagedMaxCtas;
+    const size_t rows = (size_t)w.pre_slots[f] * w.pre_rows[f];
+    if (rows > pre_slot_rows) pre_slot_rows = rows;
+  }
   w.off_seg = 0;
   w.off_own_ml = align256((size_t)w.own_items * sizeof(int2));
   w.off_own_o = w.off_own_ml + align256((size_t)w.own_slots * w.slot_rows * sizeof(float2));
   w.off_pre_ml = w.off_own_o + align256((size_t)w.own_slots * w.slot_rows * d * sizeof(float));
-  w.off_pre_o = w.off_pre_ml + align256((size_t)w.pre_slots * w.item_rows * sizeof(float2));
-  w.total = w.off_pre_o + align256((size_t)w.pre_slots * w.item_rows * d * sizeof(float));
+  w.off_pre_o = w.off_pre_ml + align256(pre_slot_rows * sizeof(float2));
+  w.total = w.off_pre_o + align256(pre_slot_rows * d * sizeof(float));
   return w;
+}
+
+// The form of the prefix items: the few-rows form reads the prefix once for every 32 rows, the dense
+// form once for every 256, but next to own items in the few-rows form it is a phase of its own (its
+// code and its first tiles, some 10 us of each CTA).  Up to 4 few-rows units per CTA are cheaper:
+// 24 sequences of 5 rows and 16 heads (d = 64) over 2000 tokens, 3.5 units each, take 63 us against 65
+// in the dense form, over 4000 tokens 68 against 67.
+inline int prefix_few(const PagedWs& w, int H_kv, int prefix_len, int few_kt) {
+  if (!w.packed || !w.own_few) return 0;
+  const long long tiles = ((long long)prefix_len + (1 << few_kt) - 1) >> few_kt;
+  return w.n_groups[1] == 1 || w.n_groups[1] * H_kv * tiles <= 4 * kPagedMaxCtas;
 }
 
 struct PagedMaps {

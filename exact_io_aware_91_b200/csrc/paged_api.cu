@@ -49,7 +49,8 @@ fa_status check_paged(const fa_paged_problem* p, bool queries, bool* empty) {
     // all (item, key tile) units, with one more per item, are counted in 32 bits
     const PagedWs w = paged_ws_layout(p->B, p->H, p->H_kv, p->T, p->d);
     const long long own = ((long long)p->max_pages * p->page_size + 63) / 64, pre = (p->prefix_len + 63ll) / 64;
-    if (w.own_items > 0x7fffffffLL / (own + pre + 1) || w.pre_items > 0x7fffffffLL / (pre + 1))
+    const long long groups = std::max(w.n_groups[0], w.n_groups[1]);
+    if (w.own_items > 0x7fffffffLL / (own + pre + 1) || groups * p->H_kv > 0x7fffffffLL / (pre + 1))
       return FA_ERR_UNSUPPORTED;
   }
   return FA_OK;
@@ -165,15 +166,17 @@ fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k
   p.causal = pr->causal;
   p.box_rows = std::min(pr->page_size, 32);
   p.packed = w.packed;
-  p.seqs = w.seqs;
   p.n_rc = w.n_rc;
-  p.n_groups = w.n_groups;
   p.own_few = w.own_few;
-  p.pre_few = w.pre_few;
   // keys per tile: 128; 64 in the dense form at d = 256 (tensor memory), 256 in the few-rows form at d = 64
   const int few_kt = d == 64 ? 8 : 7, dense_kt = d == 256 ? 6 : 7;
+  p.pre_few = prefix_few(w, p.H_kv, p.prefix_len, few_kt);
+  p.seqs = w.packed ? w.seqs[p.pre_few] : 1;
+  p.group_seqs = w.group_seqs[p.pre_few];
+  p.n_groups = w.n_groups[p.pre_few];
+  p.pre_rows = w.pre_rows[p.pre_few];
   p.own_kt = w.own_few ? few_kt : dense_kt;
-  p.pre_kt = w.pre_few ? few_kt : dense_kt;
+  p.pre_kt = p.pre_few ? few_kt : dense_kt;
   p.pre_tiles = (pr->prefix_len + (1 << p.pre_kt) - 1) >> p.pre_kt;
   p.ctas = std::min(num_sms, kPagedMaxCtas);
   p.scale_log2 = pr->scale * 1.4426950408889634f;

@@ -148,6 +148,14 @@ def test_many_sequences_share_the_prefix():
     case(list(rng.integers(0, 9, 7)), 260, 33, 1, 2, 128, 32)   # 66 rows each
 
 
+@pytest.mark.parametrize("d,prefix", [(64, 6100), (128, 3100), (256, 3100)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_a_long_prefix_for_many_sequences(d, prefix, dtype):
+    # enough (rows, key tile) pairs that the prefix takes the 128-row products, the sequences' own keys do not
+    rng = np.random.default_rng(d)
+    case([int(x) for x in rng.integers(-1, 40, 100)], prefix, 16, 4, 1, d, 32, dtype)
+
+
 def test_sharp_rows():
     case([900, 40, 1500], 800, 8, 2, 1, 128, 16, BF16, spiky=0.01)
     case([900, 40, 1500], 800, 8, 2, 1, 128, 16, F16, spiky=0.01)
