@@ -382,8 +382,9 @@ typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
  * Query head h reads key/value head h / (H / H_kv).  A query that sees no key gets o = 0 and
  * lse = -inf.  Rows with seq_lens[b] < 0 are left as they were in o and lse.  Whatever lies in
  * pages behind a sequence's last token (or behind prefix_len), infinities and NaN included, does
- * not reach the outputs.  A visible key, value or query that is not finite, or a score beyond the
- * fp32 range, makes its rows unspecified (FA_ERR_RANGE from fa_last_device_status).
+ * not reach the outputs.  A query that is not finite, or a score beyond the fp32 range, makes its row
+ * unspecified; a key or value that is not finite and that some query sees, all rows of its sequence
+ * (of the batch, in the prefix).  FA_ERR_RANGE from fa_last_device_status tells.
  * Products run in `dtype` with fp32 accumulation, the softmax in fp32; the probabilities are
  * rounded to `dtype` for the P V product (the row sum takes the rounded values), and o once at
  * the end.  d is 64, 128 or 256.  The result does not depend on timing: partial sums are joined
