@@ -1472,10 +1472,10 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   constexpr int ITEM = 128 * Dense<D>::NWG;
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);  // (b * H + h) * T + t
-  if (row >= (long long)p.B * p.H * p.T) return;
-  const long long bk = row / p.R;  // b * H_kv + hk
-  const int r = (int)(row - bk * p.R), b = (int)(bk / p.H_kv), hk = (int)(bk - (long long)b * p.H_kv);
+  const int row = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5);  // (b * H + h) * T + t, fewer than 2^30
+  if (row >= p.B * p.H * p.T) return;
+  const int bk = (int)((unsigned)row / (unsigned)p.R);  // b * H_kv + hk
+  const int r = row - bk * p.R, b = (int)((unsigned)bk / (unsigned)p.H_kv), hk = bk - b * p.H_kv;
   const int len = own_len(p, b);
   if (len < 0) return;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
@@ -1511,50 +1511,62 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.f;
+  constexpr int V = E == 2 ? 2 : 4, G = 4;  // floats per load; parts in flight (8: fewer warps fit, 4 us more at 10 parts)
   for (int i0 = 0; i0 < n; i0 += 32) {
+    const int m32 = min(32, n - i0);
     float2 ml = make_float2(-INFINITY, 0.f);
     long long where = 0;
-    if (i0 + lane < n) {
+    if (lane < m32) {
       where = at(i0 + lane);
       ml = (i0 + lane < n_own ? p.own_ml : p.pre_ml)[where];
     }
-    float m = ml.x;
+    float c = 0.f;
+    for (int k0 = 0; k0 < m32; k0 += G) {
+      // O is on its way before the weights are known
+      float v[G][E];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float mn = fmaxf(M, m);
-    const float a = mn == -INFINITY ? 0.f : ex2_approx(M - mn);
-    const float c = mn == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
-    float s = c * ml.y;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    L = fmaf(L, a, s);
-    M = mn;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] *= a;
-    const int m32 = min(32, n - i0);
-    for (int k0 = 0; k0 < m32; k0 += 4) {  // four parts' loads in flight
-      float2 v[4][E / 2];
-      float ck[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        ck[k] = __shfl_sync(0xffffffffu, c, k0 + k);
+      for (int k = 0; k < G; ++k) {
         const long long wk = __shfl_sync(0xffffffffu, where, k0 + k);
         const float* src = (i0 + k0 + k < n_own ? p.own_o : p.pre_o) + wk * D + lane * E;
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i)
-          v[k][i] = k0 + k < m32 ? *reinterpret_cast<const float2*>(src + 2 * i) : make_float2(0.f, 0.f);
+        for (int i = 0; i < E; i += V) {
+          if (k0 + k >= m32) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[k][i + e] = 0.f;
+          } else if constexpr (V == 2) {
+            const float2 x = *reinterpret_cast<const float2*>(src + i);
+            v[k][i] = x.x, v[k][i + 1] = x.y;
+          } else {
+            const float4 x = *reinterpret_cast<const float4*>(src + i);
+            v[k][i] = x.x, v[k][i + 1] = x.y, v[k][i + 2] = x.z, v[k][i + 3] = x.w;
+          }
+        }
+      }
+      if (k0 == 0) {
+        float m = ml.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float mn = fmaxf(M, m);
+        const float a = mn == -INFINITY ? 0.f : ex2_approx(M - mn);
+        c = mn == -INFINITY ? 0.f : ex2_approx(ml.x - mn);
+        float s = c * ml.y;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        L = fmaf(L, a, s);
+        M = mn;
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] *= a;
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < G; ++k) {
+        const float ck = __shfl_sync(0xffffffffu, c, k0 + k);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) {
-          o[2 * i] = fmaf(ck[k], v[k][i].x, o[2 * i]);
-          o[2 * i + 1] = fmaf(ck[k], v[k][i].y, o[2 * i + 1]);
-        }
+        for (int i = 0; i < E; ++i) o[i] = fmaf(ck, v[k][i], o[i]);
+      }
     }
   }
   const float inv = L > 0.f ? 1.0f / L : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + (row * D + lane * E) * 2);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + ((size_t)row * D + lane * E) * 2);
 #pragma unroll
   for (int i = 0; i < E; i += 2) dst[i / 2] = pack16<BF>(o[i] * inv, o[i + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
