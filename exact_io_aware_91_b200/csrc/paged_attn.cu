@@ -147,7 +147,7 @@ struct Smem {
   static constexpr int SEG_EMPTY = SEG_FULL + kSegRing, NBAR = SEG_EMPTY + kSegRing;
   static constexpr int OFF_SEG = OFF_BAR + NBAR * 8;
   static constexpr int OFF_START = OFF_SEG + kSegRing * (int)sizeof(Seg);
-  static constexpr int OFF_SCAN = OFF_START + 48;  // long long[12]
+  static constexpr int OFF_SCAN = OFF_START + 48;  // int[12]
   static constexpr int OFF_TMEM_SLOT = OFF_SCAN + 96;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 8;
   static constexpr int OFF_ISSUED = OFF_ABORT + 8;  // uint32[2]: ring index behind the last K and V slot asked for
@@ -244,6 +244,13 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
   }
+}
+// Keeps every use of loaded registers behind the wait for them (the compiler knows of no tie between
+// a load and the wait).
+template <int N>
+__device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[N]) {
@@ -555,6 +562,8 @@ __device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, 
     for (int c = 0; c < KT / 32; ++c) tmem_ld32(tS + 32 * c, u[c]);
     tmem_wait_ld();
 #pragma unroll
+    for (int c = 0; c < KT / 32; ++c) loaded(u[c]);
+#pragma unroll
     for (int c = 0; c < KT / 32; ++c)
 #pragma unroll
       for (int i = 0; i < 32; ++i) x[32 * c + i] = __uint_as_float(u[c][i]);
@@ -583,6 +592,7 @@ __device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, 
       uint32_t u[32];
       tmem_ld32(tO + 32 * c, u);
       tmem_wait_ld();
+      loaded(u);
 #pragma unroll
       for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
       tmem_st32(tO + 32 * c, u);
@@ -886,11 +896,14 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
             uint32_t v[32];
             tmem_ld32(tO2 + 32 * c, v);
             tmem_wait_ld();
+            loaded(u);
+            loaded(v);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               u[i] = __float_as_uint(fmaf(ca, __uint_as_float(u[i]), cb * __uint_as_float(v[i])));
           } else {
             tmem_wait_ld();
+            loaded(u);
 #pragma unroll
             for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(ca * __uint_as_float(u[i]));
           }
@@ -1003,6 +1016,8 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
       for (int g = 0; g < KPT; ++g) tmem_ld<N>(tmem + lanes + L::T_S(n & 3u, g), u[g]);
       tmem_wait_ld();
 #pragma unroll
+      for (int g = 0; g < KPT; ++g) loaded(u[g]);
+#pragma unroll
       for (int g = 0; g < KPT; ++g)
 #pragma unroll
         for (int r = 0; r < N; ++r) s[g][r] = __uint_as_float(u[g][r]);
@@ -1063,6 +1078,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
           uint32_t u[N];
           tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u);
           tmem_wait_ld();
+          loaded(u);
 #pragma unroll
           for (int r = 0; r < N; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * a[r]);
           tmem_st<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u);
@@ -1112,6 +1128,8 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
 #pragma unroll
   for (int h = 0; h < L::PARTS_D; ++h) tmem_ld<N>(tmem + lanes + L::T_O(seg_no & 1u, h), u[h]);
   tmem_wait_ld();
+#pragma unroll
+  for (int h = 0; h < L::PARTS_D; ++h) loaded(u[h]);
   tc_fence_before();
   mbar_arrive(bar(L::O_FREE + (seg_no & 1u)));
   const bool write = D >= 128 || key < D;
