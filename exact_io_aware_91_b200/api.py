@@ -715,8 +715,9 @@ def fa_pages_workspace_size(rows: int, num_pages: int) -> int:
 
 
 def _planes(planes) -> tuple[bytes, object, torch.device]:
-    """``fa_page_planes`` (and the array of addresses that it points to) of one (n_planes, num_pages, ...) tensor or of a sequence of
-    (num_pages, ...) tensors of one shape, type and layout; each page is dense."""
+    """``fa_page_planes`` (and the array of addresses that it points to) of one (n_planes,
+    num_pages, ...) tensor or of a sequence of (num_pages, ...) tensors of one shape, type and
+    layout; each page is dense."""
     if isinstance(planes, torch.Tensor):
         x, shape, strides = planes, planes.shape[1:], planes.stride()[1:]
         if planes.dim() < 3 or not planes.shape[0]:
@@ -745,6 +746,8 @@ def _planes(planes) -> tuple[bytes, object, torch.device]:
         size *= shape[i]
     pages = shape[0]
     step = strides[0] if pages > 1 else size
+    if not size:  # strides and addresses of empty tensors say nothing
+        step, ptrs = 0, [None] * len(ptrs)
     if step < size:
         raise ValueError("planes: pages must not overlap")
     device = _cuda_device(x)

@@ -441,13 +441,14 @@ __global__ void __launch_bounds__(256) fa_pages_compact_apply_kernel(const Table
   }
 }
 
-// Pieces of `target` bytes at least, so that `units` pages fill the device.
+// Pieces of `target` bytes or less, one at least (a page may have no bytes, or a call no planes).
 Chunks cut(int n_planes, long long page_bytes, long long page_stride, long long target) {
   Chunks c{};
   c.page_bytes = page_bytes;
   c.page_stride = page_stride;
   c.n_planes = n_planes;
   c.per_page = (int)((page_bytes + target - 1) / target);
+  if (c.per_page < 1) c.per_page = 1;
   c.piece = ((page_bytes + c.per_page - 1) / c.per_page + 15) & ~15ll;
   return c;
 }
@@ -468,7 +469,8 @@ cudaError_t launch_pages_copy(const PlanePtrs& pl, int n_planes, long long page_
   // enough blocks to fill the device eight deep, not more: each of them reads the whole list
   const long long pieces = (long long)n_planes * c.per_page;
   long long y = (8ll * num_sms + n - 1) / n;
-  y = y < 1 ? 1 : y > pieces ? pieces : y;
+  y = y > pieces ? pieces : y;
+  y = y < 1 ? 1 : y;  // without pieces the list is checked all the same
   fa_pages_copy_kernel<<<dim3(n, (unsigned)(y < 65535 ? y : 65535)), 256, 0, s>>>(pl, c, src, dst, n, num_pages, err);
   return cudaGetLastError();
 }

@@ -1,6 +1,8 @@
 """The page operations (fa_pages_*) on the GPU against their plain definitions: tables, lengths and
 counts are whole numbers and contents are copied, so everything has to be equal."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -292,3 +294,48 @@ def test_the_binding_refuses_what_does_not_fit():
         api.fa_pages_compact(c.pool[:, :10], *c.args())
     with pytest.raises(api.FAError):
         api.fa_pages_free(12, *c.args()[1:], one)
+
+
+@pytest.mark.parametrize("n_planes,page_bytes", [(0, 0), (0, 96), (2, 0)])
+def test_tables_alone(n_planes, page_bytes):
+    """No planes, or pages without bytes: tables and counts change as ever, and lists are checked."""
+    c = Both(4, 6, 20)
+    lib, stream = api.library(), torch.cuda.current_stream().cuda_stream
+    ptrs = (ctypes.c_void_p * 2)(c.pool.data_ptr(), c.pool.data_ptr())
+    pl = api.FaPagePlanes(ctypes.cast(ptrs, ctypes.POINTER(ctypes.c_void_p)), n_planes, 20, page_bytes, page_bytes)
+    t = api.FaPageTable(4, 6, c.table.stride(0), c.ps, 20, c.table.data_ptr(), c.lens.data_ptr(), c.refs.data_ptr())
+    ws = torch.empty(api.fa_pages_workspace_size(4, 20), dtype=torch.uint8, device="cuda")
+    pl, t = ctypes.byref(pl), ctypes.byref(t)
+    c.reserve([20, -1, -1, 8])
+    par, chi, old, new = i32([0, 3]), i32([1, 2]), i32([0, 25]), i32([7, 3])
+    assert lib.fa_pages_fork(pl, t, par.data_ptr(), chi.data_ptr(), 2, ws.data_ptr(), ws.numel(), stream) == api.FA_OK
+    c.o.fork([0, 3], [1, 2])
+    c.o.content = list(range(20))  # nothing is copied
+    c.check()
+    c.free([0])
+    out = torch.empty(20, dtype=torch.int32, device="cuda")
+    assert lib.fa_pages_compact(pl, t, c.table.data_ptr(), c.refs.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                                ws.numel(), stream) == api.FA_OK
+    assert out.tolist() == c.o.compact()
+    c.o.content = list(range(20))
+    c.check()
+    assert lib.fa_pages_copy(pl, old.data_ptr(), new.data_ptr(), 2, stream) == api.FA_OK
+    assert api.fa_last_device_status() == api.FA_ERR_INDEX
+    c.check()
+
+
+def test_pages_without_elements_and_pools_without_pages():
+    c = Both(4, 6, 20)
+    empty = torch.empty(2, 20, 0, dtype=torch.bfloat16, device="cuda")
+    c.reserve([20, -1, -1, 8])
+    api.fa_pages_fork(empty, *c.args(), i32([0, 3]), i32([1, 2]))
+    c.o.fork([0, 3], [1, 2])
+    c.o.content = list(range(20))
+    c.check()
+    api.fa_pages_copy(empty, i32([0, 1]), i32([7, 8]))
+    c.check()
+    api.fa_pages_copy(c.pool[:, :0], i32([-1, 2]), i32([3, 2]))  # skipped, both of them
+    assert api.fa_last_device_status() == api.FA_OK
+    api.fa_pages_copy(c.pool[:, :0], i32([1]), i32([0]))
+    assert api.fa_last_device_status() == api.FA_ERR_INDEX
+    Both(3, 2, 0).reserve([4, -1, 0])  # nobody is served
