@@ -970,8 +970,8 @@ __device__ __forceinline__ float group_join(const float (&v)[N], int lane, int w
 // A warpgroup's work on one segment with up to N rows (N = 4, 8, 16 or 32): thread k has key k of
 // every tile and, in the end, column k of O.  False (for all threads) if a bounded wait gave up.
 template <int D, bool BF, int N>
-__device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg, uint32_t bars,
-                                            uint32_t base, uint8_t* gbase, uint32_t tmem, const Waits& wctx, int w, uint32_t kv,
+__device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg, uint32_t bars, uint32_t base,
+                                            uint8_t* gbase, uint32_t tmem, const Waits& wctx, int w, uint32_t kv,
                                             uint32_t seg_no, uint32_t& s_no) {
   using L = Few<D>;
   constexpr uint32_t NS = L::NS;
@@ -1235,7 +1235,8 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
     };
     int t = 0, n_tiles = 0;
     uint32_t n_s = 0, seg_no = 0xffffffffu, cols = 0;
-    uint32_t s_no0 = 0, s_no1 = 0;  // steps of each warpgroup: it waits for its own only, so they have their own barriers
+    // steps of each warpgroup: it waits for its own only, so they have their own barriers
+    uint32_t s_no0 = 0, s_no1 = 0;
     bool more = true;
     auto issue_s = [&]() -> Step {
       Step f{};
@@ -1313,8 +1314,8 @@ __device__ __forceinline__ void few_feed(const PagedMaps& maps, const PagedParam
 
 // Warps 4 - 11: softmax, the two warpgroups take segments in turn.
 template <int D, bool BF>
-__device__ __forceinline__ void few_softmax(const PagedParams& p, SegRing& segs, uint32_t base, uint8_t* gbase, uint32_t bars,
-                                            uint32_t tmem, const Waits& wctx) {
+__device__ __forceinline__ void few_softmax(const PagedParams& p, SegRing& segs, uint32_t base, uint8_t* gbase,
+                                            uint32_t bars, uint32_t tmem, const Waits& wctx) {
   Seg sg;
   const int w = (int)(threadIdx.x >> 7) - 1;
   uint32_t kv = 0, seg_no = 0, s_no = 0;
@@ -1495,8 +1496,10 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   const int bk = (int)((unsigned)row / (unsigned)p.R);  // b * H_kv + hk
   const int r = row - bk * p.R, b = (int)((unsigned)bk / (unsigned)p.H_kv), hk = bk - b * p.H_kv;
   const int len = own_len(p, b);
+  // The parts are written.  Rows without a sequence wait too: a grid of them alone would otherwise end,
+  // and the stream's next kernel begin, while the prefix items still write their parts.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (len < 0) return;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
   const int rc = r / ITEM;
   const int nt = own_tiles(p, len, own_visible<ITEM>(p, len, rc));
   const bool pre = p.packed && p.prefix_len > 0;
@@ -1529,7 +1532,8 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) o[i] = 0.f;
-  constexpr int V = E == 2 ? 2 : 4, G = 4;  // floats per load; parts in flight (8: fewer warps fit, 4 us more at 10 parts)
+  // floats per load; parts in flight (8: fewer warps fit, 4 us more at 10 parts)
+  constexpr int V = E == 2 ? 2 : 4, G = 4;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int m32 = min(32, n - i0);
     float2 ml = make_float2(-INFINITY, 0.f);

@@ -318,3 +318,25 @@ def test_the_binding_refuses_what_does_not_fit():
     for change in (dict(prefix_len=-1), dict(scale=0.0), dict(workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(api.FAError):
             api.fa_paged_attn(**{**good, **change})
+
+
+def test_a_batch_without_sequences_ends_before_what_follows_it():
+    """Nobody wants the results, but the prefix parts of such a call are written: the next call on its
+    workspace, or a write to the pages, must not meet them."""
+    c = Cache([40, 9, 130, 64] * 8, 6000, 2, 128, 16, BF16)
+    q = c.queries(8, 1)
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()  # noqa: E731
+    table, lens, prefix, dead = dev(c.table), dev(c.lens), dev(c.prefix), dev([-1] * 32)
+    ws = torch.empty(api.fa_paged_attn_workspace_size(api.paged_problem(q, c.k, c.v, table, 6000)),
+                     dtype=torch.uint8, device="cuda")
+    args = dict(block_table=table, prefix_table=prefix, prefix_len=6000)
+    want, want_lse = api.fa_paged_attn(q, c.k, c.v, seq_lens=lens, **args)
+    other, rest = torch.full_like(q, 3.0), torch.full_like(want, 7.0)
+    rest_lse = torch.full_like(want_lse, 7.0)
+    got = []
+    for _ in range(20):
+        api.fa_paged_attn(other, c.k, c.v, seq_lens=dead, workspace=ws, o=rest, lse=rest_lse, **args)
+        got.append(api.fa_paged_attn(q, c.k, c.v, seq_lens=lens, workspace=ws, **args))
+    for o, lse in got:
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert bool((rest == 7.0).all()) and bool((rest_lse == 7.0).all())
