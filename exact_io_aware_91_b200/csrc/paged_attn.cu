@@ -1438,8 +1438,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // False if a wait gave up: the CTA ends then.
   auto phase_end = [&](bool few) -> bool {
     __syncwarp();
+    // The phases share the ring and tensor memory: what a thread wrote to shared memory last (the few-rows
+    // form's row sums lie where the dense form at d = 128 and 256 has a ring slot) comes before the next
+    // phase's copies, which a barrier alone does not order.
+    fence_proxy_async_smem();
     tc_fence_before();
-    __syncthreads();  // the phases share the ring and tensor memory
+    __syncthreads();
     tc_fence_after();
     if (!*abort_flag) return true;
     if (threadIdx.x == 0) {
