@@ -153,6 +153,13 @@ inline PagedWs paged_ws_layout(int B, int H, int H_kv, int T, int d) {
   return w;
 }
 
+// Whether an own item's note of its parts (PagedParams::seg) names parts of the line at all.  A CTA that
+// gave up a wait leaves the notes of its items unwritten: they are what the workspace held before, and the
+// joining kernel must not go where they point.
+__host__ __device__ inline bool parts_known(int first, int last, int ctas) {
+  return 0 <= first && first <= last && last < ctas;
+}
+
 // The form of the prefix items: the few-rows form reads the prefix once for every 32 rows, the dense
 // form once for every 256, but next to own items in the few-rows form it is a phase of its own (its
 // code and its first tiles, some 10 us of each CTA).  Up to 4 few-rows units per CTA are cheaper:

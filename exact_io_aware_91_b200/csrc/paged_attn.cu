@@ -1511,6 +1511,7 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
   int2 own = make_int2(0, -1), pc = make_int2(0, -1);
   if (nt > 0) {
     own = p.seg[item];
+    if (!parts_known(own.x, own.y, p.ctas)) return;  // after a wait that gave up, which is reported
     if (own.x == own.y && !pre) return;  // written at once
   }
   int pre_item = 0, pre_row = 0;
