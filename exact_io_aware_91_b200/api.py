@@ -35,7 +35,7 @@ EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_workspace_size", "fa_fwd_ws", "fa_fwd
            "fa_attn_fwd_fp8_workspace_size", "fa_attn_fwd_fp8", "fa_bwd_noalloc", "fa_last_device_status",
            "fa_paged_attn_workspace_size", "fa_paged_attn", "fa_pages_write", "fa_pages_workspace_size", "fa_pages_copy",
            "fa_pages_reserve", "fa_pages_fork", "fa_pages_free", "fa_pages_compact",
-           "fa_device_status", "fa_bwd_set_phase_events", "fa_selftest_wait_timeout", "fa_selftest_exp2",
+           "fa_device_status", "fa_bwd_set_phase_events", "fa_selftest_wait_timeout", "fa_selftest_paged_give_up", "fa_selftest_exp2",
            "fa_status_str")
 
 # Size of the scratch array fa_bwd_noalloc uses instead of a caller workspace.
@@ -149,6 +149,8 @@ def library() -> ctypes.CDLL:
     lib.fa_pages_free.restype = i
     lib.fa_pages_compact.argtypes = [pl, pt, vp, vp, vp, vp, sz, vp]
     lib.fa_pages_compact.restype = i
+    lib.fa_selftest_paged_give_up.argtypes = [pg, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, vp]
+    lib.fa_selftest_paged_give_up.restype = i
     lib.fa_selftest_wait_timeout.argtypes = [vp]
     lib.fa_selftest_wait_timeout.restype = i
     lib.fa_selftest_exp2.argtypes = [vp, vp, i, vp]
@@ -846,6 +848,21 @@ def fa_selftest_wait_timeout(stream=None) -> None:
     """Enqueue the bounded-wait self-test (a wait that must give up after ~2 s and report
     FA_ERR_TIMEOUT through ``fa_device_status``)."""
     _check("fa_selftest_wait_timeout", library().fa_selftest_wait_timeout(_stream_handle(stream)))
+
+
+def fa_selftest_paged_give_up(q, k_pages, v_pages, block_table, seq_lens, prefix_table, prefix_len: int, o, lse,
+                              workspace, segment: int, causal: bool = True, stream=None) -> None:
+    """Enqueue ``fa_paged_attn`` with waits that give up from a CTA's part ``segment`` (>= 1) on (C
+    ``fa_selftest_paged_give_up``)."""
+    device, shape = _cuda_device(q), q.shape
+    pr = _attn_problem(q, k_pages, v_pages, block_table, shape, prefix_len, causal, None, device)
+    ws, ws_bytes = _workspace_args(workspace, device)
+    _check("fa_selftest_paged_give_up", _launch_on(
+        device, stream, library().fa_selftest_paged_give_up, pr, _dense("q", q, q.dtype, shape, device),
+        k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), _int32("seq_lens", seq_lens, device, shape[0]),
+        None if prefix_table is None else _int32("prefix_table", prefix_table, device),
+        _dense("o", o, q.dtype, shape, device), _dense("lse", lse, torch.float32, shape[:3], device), ws, ws_bytes,
+        segment))
 
 
 def fa_selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:

@@ -96,6 +96,7 @@ struct PagedParams {
   int own_kt, pre_kt;  // log2 of the keys per tile
   int pre_tiles;   // key tiles of the prefix
   int ctas;        // grid
+  int give_up;     // self-test: n > 0 raises a CTA's abort flag at its n-th segment
   float scale_log2;
   // partial results (unnormalised O, and the maximum and sum of each row), see PagedWs
   int2* seg;       // own items: first and last part of the line that holds the item

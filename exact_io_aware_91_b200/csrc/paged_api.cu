@@ -119,19 +119,10 @@ fa_status check_ws(const void* ws, size_t bytes, size_t need) {
   return aligned(ws, 256) ? FA_OK : FA_ERR_MISALIGNED;
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t fa_paged_attn_workspace_size(const fa_paged_problem* pr) {
-  bool empty = false;
-  if (check_paged(pr, true, &empty) != FA_OK || empty) return 0;
-  return paged_ws_layout(pr->B, pr->H, pr->H_kv, pr->T, pr->d).total;
-}
-
-fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k_pages, const void* v_pages,
-                        const int* block_table, const int* seq_lens, const int* prefix_table, void* o, float* lse,
-                        void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+// fa_paged_attn; with give_up = n > 0 every CTA that has n segments gives up its waits from the n-th on.
+fa_status paged_attn(const fa_paged_problem* pr, const void* q, const void* k_pages, const void* v_pages,
+                     const int* block_table, const int* seq_lens, const int* prefix_table, void* o, float* lse,
+                     void* workspace, size_t workspace_bytes, fa_stream_t stream, int give_up) {
   bool empty = false;
   fa_status st = check_paged(pr, true, &empty);
   if (st != FA_OK || empty) return st;
@@ -179,6 +170,7 @@ fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k
   p.pre_kt = p.pre_few ? few_kt : dense_kt;
   p.pre_tiles = (pr->prefix_len + (1 << p.pre_kt) - 1) >> p.pre_kt;
   p.ctas = std::min(num_sms, kPagedMaxCtas);
+  p.give_up = give_up;
   p.scale_log2 = pr->scale * 1.4426950408889634f;
   p.seg = reinterpret_cast<int2*>(ws + w.off_seg);
   p.own_ml = reinterpret_cast<float2*>(ws + w.off_own_ml);
@@ -209,6 +201,32 @@ fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k
       !make_tmap_4d(&maps.k, kb, bf, kd, ks, kv_box) || !make_tmap_4d(&maps.v, vb, bf, kd, vs, kv_box))
     return FA_ERR_CUDA;
   return to_status(launch_paged_attn(maps, p, d, pr->dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_paged_attn_workspace_size(const fa_paged_problem* pr) {
+  bool empty = false;
+  if (check_paged(pr, true, &empty) != FA_OK || empty) return 0;
+  return paged_ws_layout(pr->B, pr->H, pr->H_kv, pr->T, pr->d).total;
+}
+
+fa_status fa_paged_attn(const fa_paged_problem* pr, const void* q, const void* k_pages, const void* v_pages,
+                        const int* block_table, const int* seq_lens, const int* prefix_table, void* o, float* lse,
+                        void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  return paged_attn(pr, q, k_pages, v_pages, block_table, seq_lens, prefix_table, o, lse, workspace, workspace_bytes,
+                    stream, 0);
+}
+
+fa_status fa_selftest_paged_give_up(const fa_paged_problem* pr, const void* q, const void* k_pages,
+                                    const void* v_pages, const int* block_table, const int* seq_lens,
+                                    const int* prefix_table, void* o, float* lse, void* workspace,
+                                    size_t workspace_bytes, int segment, fa_stream_t stream) {
+  if (segment < 1) return FA_ERR_INVALID_ARG;
+  return paged_attn(pr, q, k_pages, v_pages, block_table, seq_lens, prefix_table, o, lse, workspace, workspace_bytes,
+                    stream, segment);
 }
 
 fa_status fa_pages_write(const fa_paged_problem* pr, const void* k, const void* v, void* k_pages, void* v_pages,

@@ -157,7 +157,8 @@ struct Smem {
 
 // mbar_wait in as few instructions as it takes (the segments' code competes for the instruction
 // cache): the same limit, on the low word of the timer, and an abort flag; the end of the phase puts
-// that into the error word.
+// that into the error word.  For whole warps: the answer is the same for all 32 threads, which go on
+// together (to instructions that need all of them) or give up together.
 struct Waits {
   uint32_t abort_flag;  // shared memory address
 };
@@ -183,7 +184,10 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Wa
       "st.volatile.shared::cta.u32 [%3], 1;\n\t"
       "FAIL:\n\t"
       "mov.u32 %0, 0;\n\t"
-      "DONE:\n\t}"
+      "DONE:\n\t"
+      "setp.ne.u32 p, %0, 0;\n\t"
+      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(w.abort_flag), "n"((uint32_t)kWaitLimitNs)
       : "memory");
@@ -495,13 +499,15 @@ struct SegRing {
 // Warp 3: the segments of a phase, and one that says that there are no more.
 template <int D>
 __device__ __forceinline__ void schedule(const PagedParams& p, const Start& start, bool pre, bool own, bool own_first,
-                                         Seg* ring, uint32_t full, uint32_t empty, uint32_t& no, const Waits& wctx) {
+                                         Seg* ring, uint32_t full, uint32_t empty, uint32_t& no,
+                                         volatile int* abort_flag, const Waits& wctx) {
   Walk<D> walk(p, start, pre, own);
   for (bool more = true; more; ++no) {
     Seg s;
     more = walk.next(s, own_first);
     s.valid = more;
     const uint32_t slot = no % kSegRing;
+    if ((int)no + 1 == p.give_up) *abort_flag = 1;  // (self-test)
     if (no >= kSegRing && !wait_bar(empty + 8u * slot, (no / kSegRing - 1) & 1u, wctx)) return;
     if ((threadIdx.x & 31) == 0) {
       ring[slot] = s;
@@ -968,7 +974,7 @@ __device__ __forceinline__ float group_join(const float (&v)[N], int lane, int w
 }
 
 // A warpgroup's work on one segment with up to N rows (N = 4, 8, 16 or 32): thread k has key k of
-// every tile and, in the end, column k of O.  False (for all threads) if a bounded wait gave up.
+// every tile and, in the end, column k of O.  False (for all threads of a warp) if a bounded wait gave up.
 template <int D, bool BF, int N>
 __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg, uint32_t bars, uint32_t base,
                                             uint8_t* gbase, uint32_t tmem, const Waits& wctx, int w, uint32_t kv,
@@ -1150,7 +1156,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
       for (int h = 0; h < L::PARTS_D; ++h)
         if (write && r < rows) dst[r * D + h * 128] = __uint_as_float(u[h][r]);
   }
-  return !group_any(id, !ok);
+  return ok;
 }
 
 // Warps 0 - 3: copies and products.
@@ -1319,14 +1325,18 @@ __device__ __forceinline__ void few_softmax(const PagedParams& p, SegRing& segs,
   Seg sg;
   const int w = (int)(threadIdx.x >> 7) - 1;
   uint32_t kv = 0, seg_no = 0, s_no = 0;
-  for (; segs.next(sg, wctx); kv += sg.t1 - sg.t0, ++seg_no) {
-    if ((seg_no & 1u) != (uint32_t)w) continue;
+  bool ok = true;
+  for (;; kv += sg.t1 - sg.t0, ++seg_no) {
+    const bool more = segs.next(sg, wctx);
+    if (more && (seg_no & 1u) != (uint32_t)w) continue;
+    // A segment has barriers among the four warps, so they take it together or not at all: where a wait
+    // gave up in one of them, this vote ends the phase for all.
+    if (group_any(1 + w, !more || !ok)) break;
     const int rows = sg.rows[0];
-    const bool ok = rows <= 4    ? few_segment<D, BF, 4>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
-                    : rows <= 8  ? few_segment<D, BF, 8>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
-                    : rows <= 16 ? few_segment<D, BF, 16>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
-                                 : few_segment<D, BF, 32>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no);
-    if (!ok) break;
+    ok = rows <= 4    ? few_segment<D, BF, 4>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
+         : rows <= 8  ? few_segment<D, BF, 8>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
+         : rows <= 16 ? few_segment<D, BF, 16>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no)
+                      : few_segment<D, BF, 32>(p, sg, bars, base, gbase, tmem, wctx, w, kv, seg_no, s_no);
   }
 }
 
@@ -1465,7 +1475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool do_own = both || (phase == 0) == own_first, do_pre = pre && (both || !do_own);
       const bool few = do_own ? p.own_few : p.pre_few;
       if (warp == 3)
-        schedule<D>(p, start, do_pre, do_own, own_first, ring, segs.full, segs.empty, segs.no, wctx);
+        schedule<D>(p, start, do_pre, do_own, own_first, ring, segs.full, segs.empty, segs.no,
+                    abort_flag, wctx);
       else if (few)
         few_feed<D, BF>(maps, p, segs, base, bars + 8u * M::FEW_BAR, tmem, asked_for, wctx);
       else

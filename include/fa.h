@@ -538,6 +538,17 @@ FA_API void fa_bwd_set_phase_events(void* const* events);
 FA_API fa_status fa_selftest_wait_timeout(fa_stream_t stream);
 
 /*
+ * fa_selftest_paged_give_up -- the same for fa_paged_attn, whose warps hand work to one another: a call of
+ * it in which every CTA that has that many parts of the work gives up its waits from part `segment`
+ * (>= 1) on, as after their limit.  It has to end, with unspecified o and lse of the sequences and FA_ERR_TIMEOUT
+ * from fa_last_device_status (if any CTA has that many parts), and leave the rest as it was.
+ */
+FA_API fa_status fa_selftest_paged_give_up(const fa_paged_problem* problem, const void* q, const void* k_pages,
+                                           const void* v_pages, const int* block_table, const int* seq_lens,
+                                           const int* prefix_table, void* o, float* lse, void* workspace,
+                                           size_t workspace_bytes, int segment, fa_stream_t stream);
+
+/*
  * fa_selftest_exp2 -- self-test of the exponential that the softmax kernels evaluate on the
  * FMA pipe for part of their probabilities (instead of the special-function unit): y[i] =
  * that function of x[i] for i < n.  x, y: device fp32 arrays, 4-byte aligned.  The function
