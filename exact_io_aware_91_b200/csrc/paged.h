@@ -37,7 +37,7 @@ inline PagesWs pages_ws_layout(int rows, int num_pages) {
   auto align256 = [](size_t x) { return (x + 255) & ~(size_t)255; };
   PagesWs w{};
   w.off_rows = 256;                                        // control block first
-  w.off_pages = w.off_rows + align256((size_t)rows * 8);   // int[2][rows]
+  w.off_pages = w.off_rows + align256((size_t)rows * 16);  // int[4][rows]
   w.total = w.off_pages + align256((size_t)num_pages * 8); // int[2][num_pages]
   return w;
 }

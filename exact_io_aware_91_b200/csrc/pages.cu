@@ -250,13 +250,29 @@ __global__ void __launch_bounds__(kPlan) fa_pages_reserve_kernel(const TableArgs
 // ---------------------------------------------------------------------------- fork
 // Workspace rows[0][i]: what the plan decided for fork i: the id of its fresh last page, kNoTail
 // when all the parent's pages are full, kLeftOut when it does not happen.  rows[1]: running need.
+// rows[2][r]: the first fork whose child is row r, rows[3][r]: whether r is the parent of one; set for the
+// rows of the list only, so that a fork is held against all others in a constant number of steps (against
+// the list itself, 2^18 forks would take 2^36 compares of this one block).
 constexpr int kNoTail = -1, kLeftOut = -2;
 
 __global__ void __launch_bounds__(kPlan) fa_pages_fork_plan_kernel(const TableArgs t, const int* __restrict__ parents,
                                                                    const int* __restrict__ children, int n, int* fresh,
-                                                                   int* before, int* ids) {
+                                                                   int* before, int* first, int* is_parent, int* ids) {
   __shared__ int smem[32];
-  __shared__ int s_par[kPlan], s_chi[kPlan];
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    const int par = parents[i], chi = children[i];
+    if (par < 0 || chi < 0) continue;
+    if (par < t.rows) first[par] = n, is_parent[par] = 0;
+    if (chi < t.rows) first[chi] = n, is_parent[chi] = 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    const int par = parents[i], chi = children[i];
+    if (par < 0 || chi < 0) continue;
+    if (par < t.rows) is_parent[par] = 1;
+    if (chi < t.rows) atomicMin(&first[chi], i);
+  }
+  __syncthreads();
   int want = 0;
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + threadIdx.x;
@@ -266,33 +282,17 @@ __global__ void __launch_bounds__(kPlan) fa_pages_fork_plan_kernel(const TableAr
       chi = children[i];
     }
     bool takes = i < n && par >= 0 && chi >= 0;
-    bool bad = false, dup = false;
     if (takes) {
-      bad = par >= t.rows || chi >= t.rows || par == chi;
+      bool bad = par >= t.rows || chi >= t.rows || par == chi;
       if (!bad) {
         const int len = t.lens[par];
         bad = len < 0 || (long long)len > ((long long)t.max_pages << t.page_shift) || t.lens[chi] > 0;
+        // a parent that is also a child, a child that is also a parent, a child forked before
+        bad = bad || first[par] < n || is_parent[chi] != 0 || first[chi] < i;
       }
+      if (bad) report(t.err, kDevIndex);
+      takes = !bad;
     }
-    // against every other fork of the list: a child forked before, a child that is also a parent,
-    // a parent that is also a child
-    for (int jb = 0; jb < n; jb += kPlan) {
-      __syncthreads();
-      const int j = jb + threadIdx.x;
-      s_par[threadIdx.x] = j < n ? parents[j] : -1;
-      s_chi[threadIdx.x] = j < n ? children[j] : -1;
-      __syncthreads();
-      const int m = min(kPlan, n - jb);
-      if (takes && !bad)
-        for (int k = 0; k < m; ++k) {
-          const int pj = s_par[k], cj = s_chi[k];
-          if (pj < 0 || cj < 0) continue;
-          if (pj == chi || cj == par) bad = true;
-          if (jb + k < i && cj == chi) dup = true;
-        }
-    }
-    if (takes && (bad || dup)) report(t.err, kDevIndex);
-    takes = takes && !bad && !dup;
     const int need = takes && (t.lens[par] & ((1 << t.page_shift) - 1)) != 0 ? 1 : 0;
     int total;
     const int ex = want + block_scan(need, &total, smem);
@@ -491,7 +491,8 @@ cudaError_t launch_pages_fork_plan(const TableArgs& t, const int* parents, const
                                    cudaStream_t s) {
   const PagesWs w = pages_ws_layout(t.rows, t.num_pages);
   int* rows = reinterpret_cast<int*>(ws + w.off_rows);
-  fa_pages_fork_plan_kernel<<<1, kPlan, 0, s>>>(t, parents, children, n, rows, rows + t.rows,
+  const size_t r = (size_t)t.rows;
+  fa_pages_fork_plan_kernel<<<1, kPlan, 0, s>>>(t, parents, children, n, rows, rows + r, rows + 2 * r, rows + 3 * r,
                                                 reinterpret_cast<int*>(ws + w.off_pages));
   return cudaGetLastError();
 }

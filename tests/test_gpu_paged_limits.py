@@ -9,6 +9,7 @@ import torch
 
 from exact_io_aware_91_b200 import api
 from test_gpu_paged import BF16, F16, Cache
+from test_gpu_pages import Both
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,52 @@ def test_giving_up_at_a_part_that_no_cta_has_changes_nothing():
     api.fa_selftest_paged_give_up(q, c.k, c.v, table, n, pre, 50, o, lse, ws, 1 << 30)
     assert api.fa_last_device_status() == api.FA_OK
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def legal(parents, children, lens):
+    """The forks that their description lets happen, each held against all others."""
+    keep = []
+    pairs = list(zip(parents, children))
+    for i, (p, c) in enumerate(pairs):
+        if p < 0 or c < 0:
+            continue
+        others = [x for j, x in enumerate(pairs) if j != i and min(x) >= 0]
+        bad = p >= len(lens) or c >= len(lens) or p == c
+        bad = bad or lens[p] < 0 or lens[c] > 0
+        bad = bad or any(x[1] == p or x[0] == c for x in others) or any(x[1] == c for x in pairs[:i] if min(x) >= 0)
+        if not bad:
+            keep.append(i)
+    return keep
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_forks_that_exclude_one_another(seed):
+    rng = np.random.default_rng(seed)
+    c = Both(30, 3, 200, 8)
+    c.reserve([int(x) if x else -1 for x in rng.integers(0, 24, 30)])
+    n = int(rng.integers(1, 31))
+    ids = lambda k: [int(x) for x in rng.integers(-2, 33, k)]  # noqa: E731
+    live, empty = ([b for b in range(30) if (c.o.lens[b] >= 0) == yes] for yes in (True, False))
+    par = [int(rng.choice(live)) if live and rng.random() < 0.8 else x for x in ids(n)]
+    chi = [int(rng.choice(empty)) if empty and rng.random() < 0.8 else x for x in ids(n)]
+    keep = legal(par, chi, c.o.lens)
+    bad = len(keep) < sum(1 for p, x in zip(par, chi) if p >= 0 and x >= 0)
+    api.fa_pages_fork(c.planes, *c.args(), i32(par), i32(chi))
+    assert api.fa_last_device_status() == (api.FA_ERR_INDEX if bad else api.FA_OK)
+    c.o.fork([par[i] for i in keep], [chi[i] for i in keep])
+    c.check()
+
+
+def test_a_quarter_of_a_million_forks():
+    n = 1 << 18
+    c = Both(2 * n, 1, 2 * n, 8, page=(8,), planes=1)
+    c.reserve([1 + b % 8 if b < n else -1 for b in range(2 * n)])  # one in eight has a full page
+    order = np.random.default_rng(0).permutation(n)
+    par, chi = i32(order), i32(np.arange(n, 2 * n))
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    api.fa_pages_fork(c.planes, *c.args(), par, chi)
+    b.record()
+    assert not c.o.fork([int(x) for x in order], list(range(n, 2 * n)))
+    c.check()
+    assert a.elapsed_time(b) < 60  # ms; each fork against every other one is some hundreds
