@@ -273,6 +273,7 @@ fa_status fa_pages_copy(const fa_page_planes* planes, const int* src, const int*
   if (st != FA_OK) return st;
   if (n < 0) return FA_ERR_INVALID_ARG;
   if (n == 0) return FA_OK;
+  if (n > (1 << 24)) return FA_ERR_UNSUPPORTED;
   if (!src || !dst) return FA_ERR_INVALID_ARG;
   if (!aligned(src, 4) || !aligned(dst, 4)) return FA_ERR_MISALIGNED;
   int num_sms = 0, *err = nullptr;

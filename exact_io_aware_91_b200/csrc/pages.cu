@@ -8,6 +8,8 @@
 // running count over ref_counts, and a single block scans 4096 counts per step without any
 // exchange between blocks.  Results are therefore the same on every run.  Counts change by
 // integer atomics, whose order does not matter.
+#include <algorithm>
+
 #include "paged.h"
 #include "sm100.cuh"
 
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(256) fa_pages_write_kernel(const WriteArgs a) 
 
 // ---------------------------------------------------------------------------- copy
 // blockIdx.x: pair; blockIdx.y: share of the pair's pieces.  Every block first looks through the
-// whole list for pairs that exclude its own: n compares against the bytes of at least one piece.
+// whole list for pairs that exclude its own.
 __global__ void __launch_bounds__(256) fa_pages_copy_kernel(const __grid_constant__ PlanePtrs pl, const Chunks c,
                                                             const int* __restrict__ src,
                                                             const int* __restrict__ dst, int n, int num_pages,
@@ -162,6 +164,68 @@ __global__ void __launch_bounds__(256) fa_pages_copy_kernel(const __grid_constan
     return;
   }
   for (int piece = blockIdx.y; piece < c.n_planes * c.per_page; piece += gridDim.y) copy_piece(pl, c, piece, s, d);
+}
+
+// The same for lists of kLongList pairs and more: a block takes `per` (at most kCopyList) consecutive pairs
+// and looks through the list once for all of them, with a hash table of their destinations; a block per
+// pair reads n^2 entries.  Measured (this form / a block per pair, us): pages of 4 KB in one plane 52 / 69
+// at 8192 pairs, 214 / 710 at 32768, 407 / 2677 at 65536; of 16 KB in four planes 411 / 355 at 16384,
+// 609 / 577 at 24576, 834 / 866 at 32768, 1665 / 2923 at 65536.
+constexpr int kLongList = 1 << 15;
+constexpr int kCopyList = 1024, kCopyTable = 2048;  // at most half full
+
+__global__ void __launch_bounds__(256) fa_pages_copy_list_kernel(const __grid_constant__ PlanePtrs pl, const Chunks c,
+                                                                 const int* __restrict__ src,
+                                                                 const int* __restrict__ dst, int n, int per,
+                                                                 int num_pages, int* err) {
+  __shared__ int s_src[kCopyList], s_dst[kCopyList];
+  // first[h]: the first of the block's pairs whose destination is key[h], -1 once a pair of the list excludes it
+  __shared__ int key[kCopyTable], first[kCopyTable];
+  const int start = blockIdx.x * per, m = min(per, n - start);
+  for (int h = threadIdx.x; h < kCopyTable; h += 256) key[h] = -1, first[h] = n;
+  __syncthreads();
+  auto hash = [](int id) -> int { return (int)(((unsigned)id * 2654435761u) >> 21); };
+  auto find = [&](int id) -> int {
+    int h = hash(id);
+    while (key[h] != id) {
+      if (key[h] < 0) return -1;
+      h = (h + 1) & (kCopyTable - 1);
+    }
+    return h;
+  };
+  for (int i = threadIdx.x; i < m; i += 256) {
+    const int s = src[start + i];
+    int d = dst[start + i];
+    if (s < 0 || s == d) d = -1;
+    if (d >= 0 && (s >= num_pages || d >= num_pages)) {
+      report(err, kDevIndex);
+      d = -1;
+    }
+    s_src[i] = s;
+    s_dst[i] = d;
+    if (d < 0) continue;
+    int h = hash(d);
+    for (int k; (k = atomicCAS(&key[h], -1, d)) != -1 && k != d;) h = (h + 1) & (kCopyTable - 1);
+    atomicMin(&first[h], i);
+  }
+  __syncthreads();
+  for (int j = threadIdx.x; j < n; j += 256) {
+    const int sj = src[j], dj = dst[j];
+    if (sj < 0 || dj < 0 || sj == dj || sj >= num_pages || dj >= num_pages) continue;
+    int h = find(sj);
+    if (h >= 0) atomicExch(&first[h], -1);
+    if (j < start && (h = find(dj)) >= 0) atomicExch(&first[h], -1);
+  }
+  __syncthreads();
+  for (int i = 0; i < m; ++i) {
+    const int d = s_dst[i];
+    if (d < 0) continue;
+    if (first[find(d)] < i) {
+      if (threadIdx.x == 0) report(err, kDevIndex);
+      continue;
+    }
+    for (int piece = 0; piece < c.n_planes * c.per_page; ++piece) copy_piece(pl, c, piece, s_src[i], d);
+  }
 }
 
 // ---------------------------------------------------------------------------- free
@@ -466,7 +530,12 @@ cudaError_t launch_pages_copy(const PlanePtrs& pl, int n_planes, long long page_
                               const int* src, const int* dst, int n, int num_pages, int num_sms, int* err,
                               cudaStream_t s) {
   const Chunks c = cut(n_planes, page_bytes, page_stride, kPiece);
-  // enough blocks to fill the device eight deep, not more: each of them reads the whole list
+  // blocks enough to fill the device eight deep, not more: each of them reads the whole list
+  if (n >= kLongList) {
+    const int per = std::min((n + 8 * num_sms - 1) / (8 * num_sms), kCopyList);
+    fa_pages_copy_list_kernel<<<(n + per - 1) / per, 256, 0, s>>>(pl, c, src, dst, n, per, num_pages, err);
+    return cudaGetLastError();
+  }
   const long long pieces = (long long)n_planes * c.per_page;
   long long y = (8ll * num_sms + n - 1) / n;
   y = y > pieces ? pieces : y;

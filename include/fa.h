@@ -450,7 +450,7 @@ typedef struct fa_page_planes {
 FA_API size_t fa_pages_workspace_size(int rows, int num_pages);
 
 /*
- * fa_pages_copy -- page dst[i] = page src[i] in every plane, i < n (device int32 arrays).  Pairs
+ * fa_pages_copy -- page dst[i] = page src[i] in every plane, i < n <= 2^24 (device int32 arrays).  Pairs
  * with a negative id are skipped, and so are pairs with src[i] = dst[i].  A pair is left out, and
  * FA_ERR_INDEX recorded, when an id is >= num_pages, when an earlier pair has the same dst, or
  * when its dst is the src of another pair (the result would depend on the order).

@@ -132,3 +132,58 @@ def test_a_quarter_of_a_million_forks():
     assert not c.o.fork([int(x) for x in order], list(range(n, 2 * n)))
     c.check()
     assert a.elapsed_time(b) < 60  # ms; each fork against every other one is some hundreds
+
+
+def copied(src, dst, pages):
+    """The pairs that the description of fa_pages_copy lets happen, and whether any is left out."""
+    pairs = [(int(s), int(d)) for s, d in zip(src, dst)]
+    used = [(s, d) for s, d in pairs if s >= 0 and d >= 0 and s != d]
+    good = [(s, d) for s, d in used if s < pages and d < pages]
+    sources, seen, done = {s for s, _ in good}, set(), []
+    for s, d in good:
+        if d not in sources and d not in seen:
+            done.append((s, d))
+        seen.add(d)
+    return done, len(done) < len(used)
+
+
+@pytest.mark.parametrize("n,clean", [(3000, True), (32767, True), (32768, True), (49999, True), (3000, False),
+                                     (32767, False), (32768, False), (49999, False), (1 << 21, False)])
+def test_long_lists_of_copies(n, clean):
+    rng = np.random.default_rng(n)
+    pages = 100000
+    c = Both(1, 1, pages, page=(8,), planes=2)
+    if clean:
+        order = rng.permutation(pages)
+        src, dst = order[:n].copy(), order[n:2 * n].copy()
+        src[7:n // 2] = src[:n // 2 - 7]  # sources more than once
+    else:  # destinations twice, near and far apart, sources that are destinations, ids out of range
+        src, dst = rng.integers(-3, pages // 2, n), rng.integers(-3, pages + 3, n)
+        src[rng.random(n) < 1e-4] = pages
+        dst[n // 2:n // 2 + 50] = dst[:50]
+        dst[101:160] = dst[100:159]
+        src[n - 40:] = dst[n // 3:n // 3 + 40]
+        src[200:220] = dst[200:220]
+    done, bad = copied(src, dst, pages)
+    api.fa_pages_copy(c.planes, i32(src), i32(dst))
+    assert api.fa_last_device_status() == (api.FA_ERR_INDEX if bad else api.FA_OK)
+    assert bad != clean
+    want = c.start.clone()
+    s, d = (torch.tensor(x, device="cuda") for x in zip(*done))
+    want[:, d] = c.start[:, s]
+    assert torch.equal(c.pool, want)
+
+
+def test_half_a_million_copies():
+    n = 1 << 19
+    c = Both(1, 1, 2 * n, page=(8,), planes=1)
+    order = torch.randperm(2 * n, device="cuda").int()
+    src, dst = order[:n].contiguous(), order[n:].contiguous()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    api.fa_pages_copy(c.planes, src, dst)
+    b.record()
+    want = c.start.clone()
+    want[:, dst.long()] = c.start[:, src.long()]
+    assert torch.equal(c.pool, want)
+    assert a.elapsed_time(b) < 60  # ms; a look through the list for each pair reads 2 TB

@@ -4,7 +4,7 @@ import ctypes
 
 
 from exact_io_aware_91_b200 import api
-from test_paged_abi import A, lib, problem  # noqa: F401
+from test_paged_abi import A, calls, lib, problem  # noqa: F401
 
 
 def give_up(lib, segment, ws_bytes=1 << 40, q=A, **change):  # noqa: F811
@@ -19,3 +19,7 @@ def test_the_self_test_refuses_what_the_call_refuses(lib):  # noqa: F811
     assert give_up(lib, 1, q=A + 8) == api.FA_ERR_MISALIGNED
     assert give_up(lib, 1, ws_bytes=0) == api.FA_ERR_INVALID_ARG
     assert give_up(lib, 1, B=0) == api.FA_OK
+
+
+def test_a_list_of_pairs_has_a_limit(lib):  # noqa: F811
+    assert calls(lib, n=(1 << 24) + 1)["copy"] == api.FA_ERR_UNSUPPORTED
