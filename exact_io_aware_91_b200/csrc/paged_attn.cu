@@ -306,8 +306,17 @@ __device__ __forceinline__ uint16_t round16(float a) {
   else
     return __half_as_ushort(__float2half_rn(a));
 }
-__device__ __forceinline__ float log_sum(float m, float l) {  // natural logarithm of 2^m l
-  return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+// Natural logarithm of 2^m l: -inf for a row that sees no key, NaN where the keys that it sees have no sum.
+__device__ __forceinline__ float log_sum(float m, float l, bool sees) {
+  return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : sees ? __int_as_float(0x7fffffff) : -INFINITY;
+}
+// Inputs that are not finite, scores and sums beyond fp32 all end in an output that is not finite (a row
+// that sees keys divides by its sum even if that is 0 or NaN).  So outputs are looked at when they are
+// written, before the rounding: `z` gathers 0 x, which is NaN for such an x.  A wrong page may be the reason
+// of one, and that report stays.
+__device__ __forceinline__ void not_finite(float& z, float x) { z = fmaf(x, 0.f, z); }
+__device__ __forceinline__ void report_range(float z, int* err) {
+  if (z != 0.f) atomicCAS(err, kDevOk, kDevRange);
 }
 
 // ---------------------------------------------------------------------------- the two lines of units
@@ -845,12 +854,6 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
                                    return true;
                                  });
           if (!ok) break;
-          // weights are at most 2^8: a sum that is no finite number came from a non-finite score
-          // (a wrong page may be the reason, and that report stays), or belongs to the row of a sequence
-          // that is not there, which may hold anything
-          if (row < live && !(l <= 3.0e38f) &&
-              (sg.own || p.lens[sg.b + tile_q * p.seqs + row / p.R] >= 0))
-            atomicCAS(p.err, kDevOk, kDevRange);
         } else {
           for (int h = 0; h < L::HALVES; ++h) mbar_arrive(bar_p + 8u * h);
         }
@@ -884,8 +887,10 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
       float ca = M == -INFINITY ? 0.f : ex2_approx(m - M);
       float cb = M == -INFINITY ? 0.f : ex2_approx(theirs.x - M);
       const float sum = ca * l + cb * theirs.y;
+      const bool sees = sg.lead > 0 || own_lim > 0;
+      float z = 0.f;
       if (sg.direct) {
-        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+        const float inv = sees ? 1.0f / sum : 0.f;
         ca *= inv;
         cb *= inv;
       }
@@ -916,6 +921,8 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
           if (write && sg.direct) {
             uint32_t h[16];
 #pragma unroll
+            for (int i = 0; i < 32; ++i) not_finite(z, __uint_as_float(u[i]));
+#pragma unroll
             for (int i = 0; i < 16; ++i)
               h[i] = pack16<BF>(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
 #pragma unroll
@@ -936,7 +943,8 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
         if (!sg.direct)
           static_cast<float2*>(sg.ml_dst)[irow] = make_float2(M, sum);
         else if (sg.ml_dst != nullptr)
-          static_cast<float*>(sg.ml_dst)[irow] = log_sum(M, sum);
+          static_cast<float*>(sg.ml_dst)[irow] = log_sum(M, sum, sees);
+        report_range(z, p.err);
       }
     }
   }
@@ -1119,14 +1127,14 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   }
   // ---- the end of the segment: row sums over the threads, then column `key` of each row
   const float total = group_join<N>(l, lane, wq, id, ex + (ex_no++ & 1u) * 32, sum_op);  // of row lane % N
-  float factor = 1.0f;
-  if (sg.direct) factor = total > 0.f ? __fdividef(1.0f, total) : 0.f;
+  // (results are written at once where the row has own keys only)
+  const bool sees = !p.causal || sg.len - p.T + lane % N % p.T >= 0;
+  const float factor = sees ? __fdividef(1.0f, total) : 0.f;
   if (key < rows) {  // (warp 0)
-    if (!(total <= 3.0e38f) && (sg.own || p.lens[sg.b + key / p.R] >= 0)) atomicCAS(p.err, kDevOk, kDevRange);
     if (!sg.direct)
       static_cast<float2*>(sg.ml_dst)[key] = make_float2(m_lane * sl2, total);
     else if (sg.ml_dst != nullptr)
-      static_cast<float*>(sg.ml_dst)[key] = log_sum(m_lane * sl2, total);
+      static_cast<float*>(sg.ml_dst)[key] = log_sum(m_lane * sl2, total, sees);
   }
   ok &= wait_bar(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
   tc_fence_after();
@@ -1141,13 +1149,19 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   const bool write = D >= 128 || key < D;
   if (sg.direct) {
     uint16_t* dst = reinterpret_cast<uint16_t*>(sg.o_dst) + key;
+    float z = 0.f;
 #pragma unroll
     for (int r = 0; r < N; ++r) {
       const float f = __shfl_sync(0xffffffffu, factor, r);
 #pragma unroll
       for (int h = 0; h < L::PARTS_D; ++h)
-        if (write && r < rows) dst[r * D + h * 128] = round16<BF>(__uint_as_float(u[h][r]) * f);
+        if (write && r < rows) {
+          const float x = __uint_as_float(u[h][r]) * f;
+          not_finite(z, x);
+          dst[r * D + h * 128] = round16<BF>(x);
+        }
     }
+    report_range(z, p.err);
   } else {
     float* dst = reinterpret_cast<float*>(sg.o_dst) + key;
 #pragma unroll
@@ -1603,12 +1617,20 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
       }
     }
   }
-  const float inv = L > 0.f ? 1.0f / L : 0.f;
+  const bool sees = p.prefix_len > 0 || (p.causal ? len - p.T + r % p.T >= 0 : len > 0);
+  const float inv = sees ? 1.0f / L : 0.f;
+  float z = 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.o) + ((size_t)row * D + lane * E) * 2);
 #pragma unroll
-  for (int i = 0; i < E; i += 2) dst[i / 2] = pack16<BF>(o[i] * inv, o[i + 1] * inv);
-  if (lane == 0 && p.lse != nullptr)
-    p.lse[row] = log_sum(M, L);
+  for (int i = 0; i < E; i += 2) {
+    o[i] *= inv;
+    o[i + 1] *= inv;
+    not_finite(z, o[i]);
+    not_finite(z, o[i + 1]);
+    dst[i / 2] = pack16<BF>(o[i], o[i + 1]);
+  }
+  report_range(z, p.err);
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = log_sum(M, L, sees);
 }
 
 template <int D, bool BF>

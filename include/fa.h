@@ -382,9 +382,12 @@ typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
  * Query head h reads key/value head h / (H / H_kv).  A query that sees no key gets o = 0 and
  * lse = -inf.  Rows with seq_lens[b] < 0 are left as they were in o and lse.  Whatever lies in
  * pages behind a sequence's last token (or behind prefix_len), infinities and NaN included, does
- * not reach the outputs.  A query that is not finite, or a score beyond the fp32 range, makes its row
- * unspecified; a key or value that is not finite and that some query sees, all rows of its sequence
- * (of the batch, in the prefix).  FA_ERR_RANGE from fa_last_device_status tells.
+ * not reach the outputs.  A score of -infinity has the weight 0.  A row is unspecified when its query is
+ * not finite, when one of its scores is +infinity or no number, or when all of them are -infinity (products
+ * beyond the fp32 range, keys that are not finite); all rows of a sequence (of the batch, in the prefix) are
+ * when a value that some query sees is not finite.  Sums of values stay inside fp32 for magnitudes up to
+ * 2^119 / (keys that a query sees); a row whose sums do not is unspecified too.  FA_ERR_RANGE from
+ * fa_last_device_status tells in each of these cases.
  * Products run in `dtype` with fp32 accumulation, the softmax in fp32; the probabilities are
  * rounded to `dtype` for the P V product (the row sum takes the rounded values), and o once at
  * the end.  d is 64, 128 or 256.  The result does not depend on timing: partial sums are joined

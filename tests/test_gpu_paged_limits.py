@@ -187,3 +187,101 @@ def test_half_a_million_copies():
     want[:, dst.long()] = c.start[:, src.long()]
     assert torch.equal(c.pool, want)
     assert a.elapsed_time(b) < 60  # ms; a look through the list for each pair reads 2 TB
+
+
+# (H, T, prefix) with two key/value heads: few rows written at once / joined; 160 rows written at once / behind
+# the prefix; 80 rows joined with a prefix in tiles of its own
+FORMS = [(8, 1, 0), (8, 3, 200), (8, 40, 0), (8, 40, 200), (8, 20, 200)]
+
+
+def place(c, b, token):
+    """Page and slot of a sequence's own token (b >= 0) or of a prefix token (b < 0)."""
+    ps = c.k.shape[2]
+    table = c.prefix if b < 0 else c.table[b]
+    return int(table[token // ps]), token % ps
+
+
+def status_of(c, q, want, **kw):
+    got = c.run(q, **kw)
+    assert api.fa_last_device_status() == want
+    return got
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("H,T,prefix", FORMS)
+def test_values_that_are_not_finite_are_reported(d, dtype, H, T, prefix):
+    c = Cache([300, 50, 44, 400], prefix, 2, d, 16, dtype, seed=d + T)
+    q = c.queries(H, T)
+    clean = status_of(c, q, api.FA_OK)
+    c.check(q, clean)
+    for pool, bad in ((c.v, np.inf), (c.v, -np.inf), (c.v, np.nan), (c.k, np.nan), (c.k, np.inf)):
+        page, slot = place(c, 0, 10)
+        keep = pool[page, 1, slot, 3].item()
+        pool[page, 1, slot, 3] = bad
+        got = status_of(c, q, api.FA_ERR_RANGE)
+        for x, y in zip(got, clean):  # the other sequences, and the heads that do not read it
+            assert torch.equal(x[1:], y[1:]) and torch.equal(x[0, :H // 2], y[0, :H // 2])
+        pool[page, 1, slot, 3] = keep
+        if prefix:
+            page, slot = place(c, -1, 5)
+            keep = pool[page, 1, slot, 3].item()
+            pool[page, 1, slot, 3] = bad
+            got = status_of(c, q, api.FA_ERR_RANGE)
+            for x, y in zip(got, clean):
+                assert torch.equal(x[:, :H // 2], y[:, :H // 2])
+            pool[page, 1, slot, 3] = keep
+    for bad in (np.inf, -np.inf, np.nan):
+        odd = q.clone()
+        odd[2, 1, T - 1, 7] = bad
+        got = status_of(c, odd, api.FA_ERR_RANGE)
+        for x, y in zip(got, clean):
+            same = torch.ones(x.shape[:3], dtype=torch.bool, device="cuda")
+            same[2, 1, T - 1] = False
+            assert torch.equal(x[same], y[same])
+    # nobody sees what a row without a sequence holds
+    c.lens[2] = -1
+    q[2] = float("nan")
+    got = status_of(c, q, api.FA_OK)
+    assert torch.equal(got[0][[0, 1, 3]], clean[0][[0, 1, 3]])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,T,prefix", FORMS)
+def test_scores_and_sums_beyond_fp32(d, H, T, prefix):
+    c = Cache([300, 50], prefix, 2, d, 16, BF16, seed=d + T + 1)
+    q = c.queries(H, T).abs() + 0.5
+    pages = [int(x) for x in c.table[0][:19]] + [int(x) for x in c.prefix]
+    # one score of -inf: the weight is 0, as it is for a score of -1000 and less
+    page, slot = place(c, 0, 10)
+    c.k[page, :, slot] = -1000.0
+    want = status_of(c, q, api.FA_OK)
+    c.k[page, :, slot] = -3e38
+    got = status_of(c, q, api.FA_OK)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # every score of a row is -inf: not a row without keys
+    k = c.k.clone()
+    c.k[pages] = -3e38
+    o, lse = status_of(c, q, api.FA_ERR_RANGE)
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    c.k.copy_(k)
+    # finite products, and a scale that takes them out of range
+    o, lse = status_of(c, q, api.FA_ERR_RANGE, scale=2e38)
+    assert torch.isnan(o).any()
+    # large values: up to 2^119 / keys they are handled, sums beyond fp32 are reported
+    zero = torch.zeros_like(q)
+    n = 300 + prefix
+    c.v[pages] = 2.0 ** (118 - int(np.log2(n)))
+    o, _ = status_of(c, zero, api.FA_OK)
+    visible = o[0, :, -1]  # the last query sees every key
+    assert torch.equal(visible, torch.full_like(visible, 2.0 ** (118 - int(np.log2(n)))))
+    c.v[pages] = 2.0 ** 127
+    status_of(c, zero, api.FA_ERR_RANGE)
+
+
+def test_rows_that_see_nothing_are_no_error():
+    for H, T, prefix in FORMS:
+        c = Cache([0, 300, 2], 0, 2, 64, 16, BF16, seed=T)
+        q = c.queries(H, T)
+        c.check(q, status_of(c, q, api.FA_OK))
+        c.check(q, status_of(c, q, api.FA_OK, causal=False), causal=False)
