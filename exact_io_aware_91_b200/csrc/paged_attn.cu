@@ -52,8 +52,11 @@
 //
 // What lies behind a sequence's last token in a page never enters: its scores are masked, and the rows of
 // the V tile are set to zero in shared memory (0 x NaN would be NaN).  P is rounded to the 16-bit
-// type for the second product (it is at most 2^8, the running maximum may lag the true one by
-// less than 8 in base 2); sums, maxima and O are fp32.
+// type for the second product; sums (of the weights before that rounding), maxima and O are fp32.
+// Weights are 2^(s - m + kShift), where the running maximum m may lag the true one by kLag.  bf16 has
+// fp32's exponents: kShift = 0, kLag = 8.  fp16 ends at 2^16 and rounds what is below 2^-25 to 0, which
+// over 10^5 keys may be some thousandths of a row's weight: kShift = 7 moves that to 2^-32, and kLag = 4
+// leaves 2^5 for the rounding of s - m where scores are large (below 2^27).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <atomic>
@@ -319,6 +322,11 @@ __device__ __forceinline__ void report_range(float z, int* err) {
   if (z != 0.f) atomicCAS(err, kDevOk, kDevRange);
 }
 
+template <bool BF>
+constexpr float kShift = BF ? 0.0f : 7.0f;
+template <bool BF>
+constexpr float kLag = BF ? 8.0f : 4.0f;
+
 // ---------------------------------------------------------------------------- the two lines of units
 // Own tokens of sequence b, at most what its row of the table holds; negative: no sequence.
 __device__ __forceinline__ int own_len(const PagedParams& p, int b) {
@@ -564,7 +572,7 @@ __device__ __forceinline__ void zero_rows(uint8_t* slot, int chunks, int chunk_b
 
 // ---------------------------------------------------------------------------- dense form: softmax step
 // One step of a row: S from tensor memory, keys from `lim` on masked, running maximum, O rescaled
-// when the maximum has moved by 2^8 or more, P back over S in parts of 64 keys (each announced on
+// when the maximum has moved by more than kLag, P back over S in parts of 64 keys (each announced on
 // its barrier, so that P V starts while the next part is computed).  `ready` waits until O may be touched.
 template <int D, bool BF, class Ready>
 __device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, int lim, bool first, float& m, float& l,
@@ -596,9 +604,9 @@ __device__ __forceinline__ bool dense_step(uint32_t tS, uint32_t tO, float sl2, 
 #pragma unroll
   for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], x[KT - 4 + i]);
   const float m_new = fmaxf(m, fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]) * sl2);
-  const float m_use = (m_new - m > 8.0f) ? m_new : m;
+  const float m_use = (m_new - m > kLag<BF>) ? m_new : m;
   const float alpha = (m_use == m) ? 1.0f : ex2_approx(m - m_use);  // 0 while nothing was visible before
-  const float neg_m = m_use == -INFINITY ? 0.0f : -m_use;           // nothing visible yet: every P is 0
+  const float neg_m = m_use == -INFINITY ? 0.0f : kShift<BF> - m_use;  // nothing visible yet: every P is 0
   if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
     if (!ready()) return false;
     tc_fence_after();
@@ -941,9 +949,9 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
       if (other) mbar_arrive(bar(L::O_FREE + (w ^ 1)));
       if (write) {
         if (!sg.direct)
-          static_cast<float2*>(sg.ml_dst)[irow] = make_float2(M, sum);
+          static_cast<float2*>(sg.ml_dst)[irow] = make_float2(M - kShift<BF>, sum);
         else if (sg.ml_dst != nullptr)
-          static_cast<float*>(sg.ml_dst)[irow] = log_sum(M, sum, sees);
+          static_cast<float*>(sg.ml_dst)[irow] = log_sum(M - kShift<BF>, sum, sees);
         report_range(z, p.err);
       }
     }
@@ -1002,9 +1010,9 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   // Rows are spread over registers where every key needs them (m, l) and over lanes where one value per
   // row is wanted: code that runs once per segment has to be short, it comes from far.  Rows behind
   // the last one compute along with whatever Q's buffer holds there; nothing reads them.
-  // Maxima are those of the unscaled scores: a weight is 2^(scale s + shift), shift = -scale max, and the
-  // maximum has moved by 2^8 once s > limit = max + 8 / scale.
-  const float sl2 = p.scale_log2, lag = fminf(8.0f / sl2, 1e30f);
+  // Maxima are those of the unscaled scores: a weight is 2^(scale s + shift), shift = kShift - scale max, and
+  // the maximum has moved by more than kLag once s > limit = max + kLag / scale.
+  const float sl2 = p.scale_log2, lag = fminf(kLag<BF> / sl2, 1e30f);
   float shift[N], limit[N], l[N];
   float m_lane = -INFINITY;  // maximum of row lane % N
 #pragma unroll
@@ -1065,7 +1073,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
       above |= top[r] > limit[r];
     }
     if (group_any(id, above)) {
-      // a maximum has moved by 2^8 or more (always on the first tile): take the tile's maxima
+      // a maximum has moved (always on the first tile): take the tile's maxima
       const float t_max = group_join<N>(top, lane, wq, id, ex + (ex_no++ & 1u) * 32, fmax_op);
       const float m_new = fmaxf(m_lane, t_max);
       const float m_use = m_new > m_lane + lag ? m_new : m_lane;
@@ -1075,7 +1083,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
       for (int r = 0; r < N; ++r) {
         const float x_r = __shfl_sync(0xffffffffu, m_use, r);
         limit[r] = x_r + lag;
-        shift[r] = x_r == -INFINITY ? 0.f : -x_r * sl2;
+        shift[r] = x_r == -INFINITY ? 0.f : fmaf(-x_r, sl2, kShift<BF>);
       }
       if (t > 0) {
         // O^T holds the earlier tiles once their products have completed
@@ -1132,9 +1140,9 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
   const float factor = sees ? __fdividef(1.0f, total) : 0.f;
   if (key < rows) {  // (warp 0)
     if (!sg.direct)
-      static_cast<float2*>(sg.ml_dst)[key] = make_float2(m_lane * sl2, total);
+      static_cast<float2*>(sg.ml_dst)[key] = make_float2(fmaf(m_lane, sl2, -kShift<BF>), total);
     else if (sg.ml_dst != nullptr)
-      static_cast<float*>(sg.ml_dst)[key] = log_sum(m_lane * sl2, total, sees);
+      static_cast<float*>(sg.ml_dst)[key] = log_sum(fmaf(m_lane, sl2, -kShift<BF>), total, sees);
   }
   ok &= wait_bar(bar(L::O_FULL + (seg_no & 1u)), seg_no / 2 & 1u, wctx);
   tc_fence_after();

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import paged_attention
 from exact_io_aware_91_b200 import api
 from test_gpu_paged import BF16, F16, Cache
 from test_gpu_pages import Both
@@ -285,3 +286,63 @@ def test_rows_that_see_nothing_are_no_error():
         q = c.queries(H, T)
         c.check(q, status_of(c, q, api.FA_OK))
         c.check(q, status_of(c, q, api.FA_OK, causal=False), causal=False)
+
+
+def check_small_weights(c, q, got, scale):
+    """As Cache.check, for fp16 weights that are multiplied by 2^7 before they are rounded: what is off by half
+    of fp16's smallest step (2^-25) is 2^-32 of a row's weight."""
+    o, lse = (x.double().cpu().numpy() for x in got)
+    O, L, mean_abs, sum_abs, big, n = paged_attention(q, c.k, c.v, c.table, c.lens, c.prefix, c.prefix_len, scale, True)
+    u = torch.finfo(c.dtype).eps / 2
+    delta = 2.0 ** -23 * (c.d * big + n + 8)
+    tol = u * np.abs(O) + (u + 2 * delta[..., None]) * mean_abs + 2.0 ** -32 * sum_abs + 2.0 ** -25
+    some = n > 0
+    assert (np.abs(o - O)[some] <= 1.001 * tol[some]).all(), (np.abs(o - O) / tol)[some].max()
+    assert (np.abs(lse[some] - L[some]) <= 2 * delta[some] + 2.0 ** -22 * np.abs(L[some])).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,T,prefix", FORMS)
+def test_small_weights_of_many_keys_count_in_fp16(d, H, T, prefix):
+    # one key with nearly all the weight and V = 0, 10^5 with weights of 2^-25.2 and V = 1, and so many sequences
+    # (of the same pages) that each one's keys lie in two or three parts
+    n = 150
+    c = Cache([100000], prefix, 2, d, 64, F16, seed=3)
+    c.k.zero_()
+    c.v.fill_(1.0)
+    page, slot = place(c, 0, 1234)
+    c.k[page, :, slot, 0] = 17.47
+    c.v[page, :, slot] = 0.0
+    q = torch.zeros(n, H, T, d, dtype=F16, device="cuda")
+    q[..., 0] = 1.0
+    one, table = q[:1], c.table
+    c.table, c.lens = np.repeat(table, n, axis=0), [100000] * n
+    o, lse = status_of(c, q, api.FA_OK, scale=1.0)
+    c.table, c.lens = table, [100000]
+    for b in (0, n - 1):
+        check_small_weights(c, one, (o[b:b + 1], lse[b:b + 1]), 1.0)
+    # the others have the same inputs: within the same bound of the first
+    assert (o.double() - o[:1].double()).abs().max() <= 2 * (2.0 ** -32 * 1e5 + 0.004 * 0.03)
+    assert (o[:, :, -1] > 0.0025).all()  # 10^5 2^-25.2 = 0.00259 in all
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,T,prefix", FORMS)
+@pytest.mark.parametrize("scale", [0.125, 1.0])
+def test_fp16_weights_of_random_keys(d, H, T, prefix, scale):
+    c = Cache([700, 33, 1500], prefix, 2, d, 16, F16, seed=d + T)
+    q = c.queries(H, T)
+    check_small_weights(c, q, status_of(c, q, api.FA_OK, scale=scale), scale)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,T,prefix", FORMS)
+def test_large_scores_stay_finite_in_fp16(d, H, T, prefix):
+    # scores up to some 2^26 in base 2, whose differences fp32 rounds to multiples of 4: one key takes each row,
+    # or several of one score, so an element of o is at most the largest of V
+    c = Cache([700, 33, 1500], prefix, 2, d, 16, F16, seed=d)
+    q = c.queries(H, T)
+    o, _ = status_of(c, q, api.FA_OK, scale=4e7 / d ** 0.5 / 6)
+    top = max(c.v[place(c, b, t)[0], :, place(c, b, t)[1]].abs().max().item()
+              for b, n in [(-1, prefix)] + list(enumerate(c.lens)) for t in range(n))
+    assert o.abs().max() <= top * (1 + 2.0 ** -10)
