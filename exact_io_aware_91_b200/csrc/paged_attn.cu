@@ -313,6 +313,13 @@ __device__ __forceinline__ uint16_t round16(float a) {
 __device__ __forceinline__ float log_sum(float m, float l, bool sees) {
   return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : sees ? __int_as_float(0x7fffffff) : -INFINITY;
 }
+// A mean of finite fp16 values, off by the rounding of its weights (2^-11), may pass fp16's end: it is that end.
+// (bf16's is as far as fp32's.)
+template <bool BF>
+__device__ __forceinline__ float to_range(float x) {
+  if constexpr (BF) return x;
+  return fabsf(x) < 65600.0f ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x;
+}
 // Inputs that are not finite, scores and sums beyond fp32 all end in an output that is not finite (a row
 // that sees keys divides by its sum even if that is 0 or NaN).  So outputs are looked at when they are
 // written, before the rounding: `z` gathers 0 x, which is NaN for such an x.  A wrong page may be the reason
@@ -932,7 +939,7 @@ __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& seg
             for (int i = 0; i < 32; ++i) not_finite(z, __uint_as_float(u[i]));
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              h[i] = pack16<BF>(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+              h[i] = pack16<BF>(to_range<BF>(__uint_as_float(u[2 * i])), to_range<BF>(__uint_as_float(u[2 * i + 1])));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(dst + c * 64 + i * 16) =
@@ -1166,7 +1173,7 @@ __device__ __forceinline__ bool few_segment(const PagedParams& p, const Seg& sg,
         if (write && r < rows) {
           const float x = __uint_as_float(u[h][r]) * f;
           not_finite(z, x);
-          dst[r * D + h * 128] = round16<BF>(x);
+          dst[r * D + h * 128] = round16<BF>(to_range<BF>(x));
         }
     }
     report_range(z, p.err);
@@ -1635,7 +1642,7 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p)
     o[i + 1] *= inv;
     not_finite(z, o[i]);
     not_finite(z, o[i + 1]);
-    dst[i / 2] = pack16<BF>(o[i], o[i + 1]);
+    dst[i / 2] = pack16<BF>(to_range<BF>(o[i]), to_range<BF>(o[i + 1]));
   }
   report_range(z, p.err);
   if (lane == 0 && p.lse != nullptr) p.lse[row] = log_sum(M, L, sees);

@@ -346,3 +346,26 @@ def test_large_scores_stay_finite_in_fp16(d, H, T, prefix):
     top = max(c.v[place(c, b, t)[0], :, place(c, b, t)[1]].abs().max().item()
               for b, n in [(-1, prefix)] + list(enumerate(c.lens)) for t in range(n))
     assert o.abs().max() <= top * (1 + 2.0 ** -10)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,T,prefix", FORMS)
+def test_a_mean_of_fp16s_largest_values_is_finite(d, H, T, prefix):
+    # one key of weight 1, the others of weights that fp16 rounds up by nearly 2^-11: off by that, the mean of
+    # V = 65504 would pass 65520, from which on fp16 rounds to infinity
+    c = Cache([2000, 40], prefix, 2, d, 16, F16, seed=d)
+    steps = np.arange(1, 300) / 64.0  # differences of scores
+    w = 2.0 ** 7 * np.exp(-steps)
+    up = steps[np.argmax(w.astype(np.float16).astype(np.float64) / w)]
+    c.k.zero_()
+    c.v.fill_(65504.0)
+    for b in ((-1, 0) if prefix else (0,)):  # a key of weight 1 in every other tile at least
+        for t in range(0, [2000, 40, prefix][b], 64):
+            page, slot = place(c, b, t)
+            c.k[page, :, slot, 0] = up
+    q = torch.zeros(2, H, T, d, dtype=F16, device="cuda")
+    q[..., 0] = 1.0
+    for sign in (1.0, -1.0):
+        o, _ = status_of(c, q, api.FA_OK, scale=1.0)
+        assert (o[0, :, -1] * sign >= 65504 * (1 - 2.0 ** -10)).all() and torch.isfinite(o).all()
+        c.v.neg_()
