@@ -664,7 +664,7 @@ __device__ __forceinline__ void dense_feed(const PagedMaps& maps, const PagedPar
                                            uint32_t bars, uint32_t tmem, volatile uint32_t* asked_for,
                                            const Waits& wctx) {
   using L = Dense<D>;
-  constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
+  constexpr int KT = L::KT, NWG = L::NWG;
   constexpr uint32_t NS = L::NS;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -817,7 +817,7 @@ template <int D, bool BF>
 __device__ __forceinline__ void dense_softmax(const PagedParams& p, SegRing& segs, uint8_t* gbase, uint32_t bars,
                                               uint32_t tmem, const Waits& wctx) {
   using L = Dense<D>;
-  constexpr int KT = L::KT, NWG = L::NWG, ITEM = 128 * NWG;
+  constexpr int KT = L::KT, NWG = L::NWG;
   constexpr uint32_t NS = L::NS;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
