@@ -165,7 +165,8 @@ __host__ __device__ inline bool parts_known(int first, int last, int ctas) {
 // form once for every 256, but next to own items in the few-rows form it is a phase of its own (its
 // code and its first tiles, some 10 us of each CTA).  Up to 4 few-rows units per CTA are cheaper:
 // 24 sequences of 5 rows and 16 heads (d = 64) over 2000 tokens, 3.5 units each, take 63 us against 65
-// in the dense form, over 4000 tokens 68 against 67.
+// in the dense form, over 4000 tokens 68 against 67.  (Measured there only; other head dims and row
+// counts have other tiles, and take the same limit.)
 inline int prefix_few(const PagedWs& w, int H_kv, int prefix_len, int few_kt) {
   if (!w.packed || !w.own_few) return 0;
   const long long tiles = ((long long)prefix_len + (1 << few_kt) - 1) >> few_kt;

@@ -23,8 +23,8 @@
 // own line first: own items wait for memory (each key is used for R rows only), prefix items for the
 // tensor core, and the two overlap across the device.  The halves are whole pairs of neighbouring
 // multiprocessors (by smid): two neighbours in different code slow each other down by fetching
-// instructions (128 sequences over a prefix of 32785 tokens: 150 us with neighbours in different lines,
-// 113 us so, 117 us with the prefix first everywhere).
+// instructions (128 sequences over a prefix of 32785 tokens, when this was chosen: 150 us with neighbours
+// in different lines, 113 us so, 117 us with the prefix first everywhere).
 //
 // Two forms of a tile's products:
 //   dense  S = Q K^T and O += P V with the query rows as the 128 rows of the product, for items of
@@ -45,10 +45,11 @@
 //
 // Measured on B200 (bf16, 32 query and 8 key/value heads, d = 128): 37 sequences of 1 to 16384 own tokens,
 // 1.24 GB of keys and values, 195 us (6.4 TB/s, 97 % of the measured copy rate), sequences of equal
-// length 6.9 TB/s; the dense form against a prefix alone 1.06 PFLOP/s for 512 sequences (65 % of the
-// measured matrix rate: a step's chain of S, softmax and P V, two of which overlap, bounds it) and 0.82 for
-// 128, where a fixed 25 us (launch, code that the instruction caches do not hold yet, cut items,
-// joining) counts; 128 sequences of 1 to 512 own tokens behind a prefix of 32785 tokens 111 us.
+// length (16384) 6.9 TB/s; the dense form against a prefix of 32785 tokens alone 256 us or 1.08 PFLOP/s for
+// 512 sequences (66 % of the measured matrix rate: a step's chain of S, softmax and P V, two of which
+// overlap, bounds it) and 85 us or 0.81 for 128, where a fixed 25 us (launch, code that the instruction
+// caches do not hold yet, cut items, joining) counts; 128 sequences of 1 to 512 own tokens behind that
+// prefix 114 us.
 //
 // What lies behind a sequence's last token in a page never enters: its scores are masked, and the rows of
 // the V tile are set to zero in shared memory (0 x NaN would be NaN).  P is rounded to the 16-bit

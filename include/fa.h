@@ -29,7 +29,7 @@
  *    device-resident error word per device (see fa_last_device_status).
  *  - Value range.  The tensor-core products that need more than bf16's 8 significant
  *    bits (P V in the forward; all products of the backward) read fp16 copies of the bf16
- *    inputs.  fp16 ends at 65504, so every copy is the input times a power of two 2^e
+ *    inputs (fa_paged_attn has none, and limits of its own, which it names).  fp16 ends at 65504, so every copy is the input times a power of two 2^e
  *    chosen from the tensor's largest magnitude (one e per tensor; per 128-key tile of V
  *    in the forward without a workspace), and the kernels undo 2^e exactly; e = 0, i.e.
  *    the plain conversion, whenever the magnitudes lie in [2^-4, 2^15].  Every finite
@@ -366,8 +366,11 @@ typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
 
 /*
  * fa_paged_attn -- attention of the newest T tokens of every sequence over its pages, with a
- * prefix that the whole batch shares (a system prompt, a document): the prefix's keys and
- * values are read once for all sequences instead of once per sequence.
+ * prefix that the whole batch shares (a system prompt, a document).  A sequence has
+ * R = H / H_kv * T query rows per key/value head.  Up to R = 128 rows of several sequences go over the
+ * prefix together, so its keys and values are read once for up to 256 rows at a time (d = 256: 128;
+ * a short prefix or few rows in all: 32) instead of once per sequence; with R above 128 each sequence
+ * reads it by itself.
  *   q, o            : (B, H, T, d) of `dtype`, 16-byte aligned, contiguous, o apart from every
  *                     input; lse: fp32 (B, H, T) or NULL.  T is 1 for decoding, more for drafts
  *                     or a prompt's chunk.
@@ -389,8 +392,9 @@ typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
  * 2^119 / (keys that a query sees); a row whose sums do not is unspecified too.  FA_ERR_RANGE from
  * fa_last_device_status tells in each of these cases.
  * Products run in `dtype` with fp32 accumulation, the softmax in fp32; the probabilities are
- * rounded to `dtype` for the P V product (the row sum takes the rounded values), and o once at
- * the end.  d is 64, 128 or 256.  The result does not depend on timing: partial sums are joined
+ * rounded to `dtype` for the P V product (bf16 keeps 8 significant bits there, where the dense entry
+ * points make fp16 copies of V and keep 11), the row sum takes them before that rounding, so lse does
+ * not feel it, and o is rounded once at the end.  d is 64, 128 or 256.  The result does not depend on timing: partial sums are joined
  * in a fixed order.
  *   workspace       : fa_paged_attn_workspace_size(problem) bytes, 256-byte aligned; contents on
  *                     entry do not matter; one call at a time per workspace.  The size depends
