@@ -11,6 +11,11 @@
 
 namespace fa {
 
+// What the kernels of the paged cache record in the error word besides the codes of sm100.cuh: an index out
+// of its range, too few free pages.  (Kept apart from the headers of the dense kernels: recorded counters
+// of those are void once their shared headers change.)
+enum : int { kDevIndex = FA_ERR_INDEX, kDevNoPages = FA_ERR_NO_PAGES };
+
 // Checks the current device; its multiprocessor count and the address of its error word.
 fa_status device_ready(int* num_sms, int** err);
 

@@ -16,9 +16,8 @@ namespace fa {
 // Device-side failures are recorded here (the host reads and clears it with
 // fa_last_device_status()): a bounded wait that ran out (kDevTimeout), or a value outside
 // what the arithmetic can represent -- a non-finite input, a score Q K^T beyond the fp32
-// range, a V element too large for the scaled fp16 copy (kDevRange); for the paged cache an
-// index out of its range (kDevIndex) or too few free pages (kDevNoPages).
-enum : int { kDevOk = 0, kDevTimeout = 5, kDevRange = 6, kDevIndex = 7, kDevNoPages = 8 };
+// range, a V element too large for the scaled fp16 copy (kDevRange).
+enum : int { kDevOk = 0, kDevTimeout = 5, kDevRange = 6 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
